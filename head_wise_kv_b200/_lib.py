@@ -32,6 +32,19 @@ DUO_KV_BF16 = 0
 DUO_KV_FP8_E4M3 = 1
 DUO_KV_INT4 = 2
 
+DUO_ROPE_HALF = 0
+DUO_ROPE_INTERLEAVED = 1
+DUO_ROPE_NONE = 0
+DUO_ROPE_LINEAR = 1
+DUO_ROPE_NTK = 2
+DUO_ROPE_YARN = 3
+DUO_ROPE_BANDS = 4
+DUO_ROPE_FACTORS = 5
+
+DUO_BF16 = 0
+DUO_FP16 = 1
+DUO_FP32 = 2
+
 DUO_STATUS_OVER_CAPACITY = 1
 DUO_STATUS_EMPTY_SEQUENCE = 2
 DUO_STATUS_WAIT_TIMEOUT = 4
@@ -47,6 +60,8 @@ EXPORTED = (
     "duo_kv_set_decode_ctas", "duo_strerror", "duo_decode_attn_static_ws",
     "duo_kv_append_rows", "duo_decode_attn_rows", "duo_lse_merge", "duo_alpha_blend", "duo_kv_set_page_table",
     "duo_kv_fork", "duo_kv_check_wait_timeout", "duo_decode_step",
+    "duo_rope_create", "duo_rope_free", "duo_rope_frequencies", "duo_rope_apply", "duo_kv_append_rope",
+    "duo_decode_step_rope", "duo_kv_pages_bytes", "duo_kv_pages_init", "duo_kv_pages_view_get", "duo_kv_reserve",
 )
 DUO_STATIC_WS_BYTES = 4 << 20
 
@@ -86,7 +101,48 @@ class duo_kv_layer_view(ctypes.Structure):
 
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
+_I64 = ctypes.c_int64
+_F64 = ctypes.c_double
 _SZ = ctypes.c_size_t
+
+
+class duo_rope_desc(ctypes.Structure):
+    _fields_ = [
+        ("head_dim", _I32),
+        ("rot_dim", _I32),
+        ("layout", _I32),
+        ("scaling", _I32),
+        ("theta", _F64),
+        ("factor", _F64),
+        ("original_len", _F64),
+        ("low", _F64),
+        ("high", _F64),
+        ("magnitude", _F64),
+        ("pair_factors", ctypes.POINTER(_F64)),
+    ]
+
+
+class duo_rope_tensor(ctypes.Structure):
+    _fields_ = [
+        ("in_", _P),
+        ("out", _P),
+        ("heads", _I32),
+        ("rotate", _I32),
+        ("in_stride", _I64 * 3),
+        ("out_stride", _I64 * 3),
+    ]
+
+
+class duo_rows(ctypes.Structure):
+    _fields_ = [("data", _P), ("token_stride", _I64), ("head_stride", _I64)]
+
+
+class duo_token_map(ctypes.Structure):
+    _fields_ = [("seq", _P), ("pos", _P), ("slot", _P), ("len_after", _P)]
+
+
+class duo_kv_pages_view(ctypes.Structure):
+    _fields_ = [("table", _P), ("held", _P), ("refs", _P), ("free_bits", _P), ("max_pages", _I32)]
 
 
 def _sig(name, args, res=ctypes.c_int):
@@ -116,6 +172,17 @@ _c_set_pages = _sig("duo_kv_set_page_table", [_P, _P, _I32])
 _c_fork = _sig("duo_kv_fork", [_P, _I32, _I32, _I32, _P])
 _c_waitcheck = _sig("duo_kv_check_wait_timeout", [_P, ctypes.c_uint64, _P])
 _c_step = _sig("duo_decode_step", [_P, _I32, _P, _P, _P, _P, _P, ctypes.c_float, _P, _P, _P, _SZ, _P])
+_c_rope_create = _sig("duo_rope_create", [ctypes.POINTER(duo_rope_desc), ctypes.POINTER(_P)])
+_c_rope_free = _sig("duo_rope_free", [_P])
+_c_rope_freq = _sig("duo_rope_frequencies", [_P, ctypes.POINTER(_F64), ctypes.POINTER(_F64)])
+_c_rope_apply = _sig("duo_rope_apply", [_P, _I32, _I32, _I32, _I32, _P, _I32, _P, _I32, _P, _P])
+_c_append_rope = _sig("duo_kv_append_rope", [_P, _I32, _P, _P, _P, _P, _P, _P, _P, _I32, _P, _P])
+_c_step_rope = _sig("duo_decode_step_rope", [_P, _I32, _P, _P, _P, _P, _P, _P, ctypes.c_float, _P, _P, _P, _P, _SZ,
+                                             _P])
+_c_pages_bytes = _sig("duo_kv_pages_bytes", [_P, _I32, ctypes.POINTER(_SZ)])
+_c_pages_init = _sig("duo_kv_pages_init", [_P, _I32, _P, _SZ, _P])
+_c_pages_view = _sig("duo_kv_pages_view_get", [_P, ctypes.POINTER(duo_kv_pages_view)])
+_c_reserve = _sig("duo_kv_reserve", [_P, _P, _P, _I32, _P, _P, _P, _P, _P, _P])
 _c_strerror = _sig("duo_strerror", [ctypes.c_int], ctypes.c_char_p)
 
 
@@ -253,3 +320,72 @@ def duo_decode_step(handle, layer, k_new, v_new, len_before, q, length, scale, o
                     workspace_bytes, stream) -> None:
     _check(_c_step(handle, layer, k_new, v_new, len_before, q, length, scale, out, lse, workspace, workspace_bytes,
                    stream), "duo_decode_step")
+
+
+def make_rope_desc(head_dim, rot_dim, layout, scaling, theta, factor=1.0, original_len=0.0, low=0.0, high=0.0,
+                   magnitude=0.0, pair_factors=None):
+    """Build a duo_rope_desc; pair_factors: optional float sequence
+    [rot_dim / 2].  The host array is kept alive by the returned pair."""
+    arr = None
+    if pair_factors is not None:
+        arr = (_F64 * len(pair_factors))(*[float(v) for v in pair_factors])
+    return duo_rope_desc(head_dim, rot_dim, layout, scaling, theta, factor, original_len, low, high, magnitude,
+                         ctypes.cast(arr, ctypes.POINTER(_F64)) if arr is not None else None), arr
+
+
+def duo_rope_create(desc) -> int:
+    h = _P()
+    _check(_c_rope_create(ctypes.byref(desc), ctypes.byref(h)), "duo_rope_create")
+    return h.value
+
+
+def duo_rope_free(handle: int) -> None:
+    _check(_c_rope_free(handle), "duo_rope_free")
+
+
+def duo_rope_frequencies(handle, rot_dim: int) -> tuple[list[float], float]:
+    f, m = (_F64 * (rot_dim // 2))(), _F64(0)
+    _check(_c_rope_freq(handle, f, ctypes.byref(m)), "duo_rope_frequencies")
+    return list(f), m.value
+
+
+def duo_rope_apply(handle, dtype, transpose, batch, n, tensors, positions, per_token, n_new, stream) -> None:
+    """tensors: a ctypes array of duo_rope_tensor."""
+    _check(_c_rope_apply(handle, dtype, transpose, batch, n, tensors, len(tensors), positions, per_token, n_new,
+                         stream), "duo_rope_apply")
+
+
+def _ref(x):
+    return ctypes.byref(x) if x is not None else None
+
+
+def duo_kv_append_rope(handle, layer, rope, q, k, v, len_before, token_map, n_new, n_tokens, q_out, stream) -> None:
+    """q, k, v: duo_rows (q may be None); token_map: duo_token_map or None."""
+    _check(_c_append_rope(handle, layer, rope, _ref(q), _ref(k), _ref(v), len_before, _ref(token_map), n_new, n_tokens,
+                          q_out, stream), "duo_kv_append_rope")
+
+
+def duo_decode_step_rope(handle, layer, rope, q, k, v, len_before, length, scale, q_rot, out, lse, workspace,
+                         workspace_bytes, stream) -> None:
+    _check(_c_step_rope(handle, layer, rope, _ref(q), _ref(k), _ref(v), len_before, length, scale, q_rot, out, lse,
+                        workspace, workspace_bytes, stream), "duo_decode_step_rope")
+
+
+def duo_kv_pages_bytes(handle, max_pages: int) -> int:
+    n = _SZ(0)
+    _check(_c_pages_bytes(handle, max_pages, ctypes.byref(n)), "duo_kv_pages_bytes")
+    return n.value
+
+
+def duo_kv_pages_init(handle, max_pages: int, dev_buf: int, buf_bytes: int, stream: int) -> None:
+    _check(_c_pages_init(handle, max_pages, dev_buf, buf_bytes, stream), "duo_kv_pages_init")
+
+
+def duo_kv_pages_view_get(handle) -> duo_kv_pages_view:
+    v = duo_kv_pages_view()
+    _check(_c_pages_view(handle, ctypes.byref(v)), "duo_kv_pages_view_get")
+    return v
+
+
+def duo_kv_reserve(handle, len_before, n_new, map_tokens, len_after, cu, seq, pos, slot, stream) -> None:
+    _check(_c_reserve(handle, len_before, n_new, map_tokens, len_after, cu, seq, pos, slot, stream), "duo_kv_reserve")

@@ -14,6 +14,22 @@ def _stream(device) -> int:
     return torch.cuda.current_stream(device).cuda_stream
 
 
+class _same_device:
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        return False
+
+
+_SAME = _same_device()
+
+
+def _on(device):
+    """torch.cuda.device, without its cost where the device is current."""
+    return _SAME if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+
 def _need(t: torch.Tensor, name: str, dtype, shape, device):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -26,6 +42,45 @@ def _need(t: torch.Tensor, name: str, dtype, shape, device):
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
+
+
+def _rows(t, name, heads, d, lead, device):
+    """A projection's rows [lead...][heads][d], bf16, token-major: duo_rows."""
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {torch.bfloat16}")
+    if tuple(t.shape) != (*lead, heads, d):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(*lead, heads, d)}")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}")
+    s = t.stride()
+    if s[-1] != 1:
+        raise ValueError(f"{name}: the elements of a head must be contiguous")
+    if len(lead) == 2 and lead[0] > 1 and lead[1] > 1 and s[0] != lead[1] * s[1]:
+        raise ValueError(f"{name}: sequences must follow one another at the token stride")
+    token = s[0] if len(lead) == 1 or lead[1] == 1 else s[1]
+    # a dimension of one row has no stride that matters
+    return L.duo_rows(t.data_ptr(), token if t.numel() > heads * d else 0, s[-2] if heads > 1 else 0)
+
+
+class TokenMap:
+    """A step's tokens on the device, as ``DuoKVCache.reserve`` writes them:
+    the sequence, position and row (slot) of each token, -1 behind the last
+    one; len_after [batch] and cu [batch + 1] (sequence b's tokens are entries
+    cu[b] .. cu[b + 1] - 1).  max_tokens: entries of the map."""
+
+    def __init__(self, batch, max_tokens, device="cuda"):
+        self.device = torch.device(device)
+        if self.device.type == "cuda" and self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
+        self.batch, self.max_tokens = int(batch), int(max_tokens)
+        if self.batch < 1 or self.max_tokens < 0:
+            raise ValueError("a map has at least one sequence and no negative number of tokens")
+
+        def make(n, dtype, value):
+            return torch.full((n,), value, dtype=dtype, device=self.device)
+        self.seq, self.pos = make(self.max_tokens, torch.int32, -1), make(self.max_tokens, torch.int32, -1)
+        self.slot = make(self.max_tokens, torch.int64, -1)
+        self.len_after, self.cu = make(self.batch, torch.int32, 0), make(self.batch + 1, torch.int32, 0)
 
 
 class DuoKVCache:
@@ -69,6 +124,7 @@ class DuoKVCache:
             self.v_scale.ravel().tolist(), page_tokens, num_pages)
         self.page_tokens, self.num_pages = page_tokens, num_pages
         self._page_table = None
+        self._page_state = None
         self.total_bytes, self.cache_bytes = L.duo_kv_required_bytes(self._desc)
         with torch.cuda.device(self.device):
             self.buf = torch.empty(self.total_bytes, dtype=torch.uint8, device=self.device)
@@ -90,6 +146,52 @@ class DuoKVCache:
             raise ValueError("page table must be a contiguous tensor on the cache's device")
         L.duo_kv_set_page_table(self.handle, table.data_ptr(), table.shape[1])
         self._page_table = table
+        self._page_state = None
+
+    def manage_pages(self, max_pages=None):
+        """Let the library keep the page table from now on, every page free:
+        ``reserve`` hands pages out and ``fork`` shares them.  max_pages: pages
+        per sequence at most (default: those of ``capacity`` tokens)."""
+        if self.page_tokens <= 0:
+            raise ValueError("manage_pages needs a paged cache")
+        n = -(-self.cap // self.page_tokens) if max_pages is None else int(max_pages)
+        with torch.cuda.device(self.device):
+            buf = torch.empty(L.duo_kv_pages_bytes(self.handle, n), dtype=torch.uint8, device=self.device)
+            L.duo_kv_pages_init(self.handle, n, buf.data_ptr(), buf.numel(), _stream(self.device))
+        self._page_state, self._page_table = buf, None
+
+    def page_state(self) -> dict:
+        """Torch views of the library's page state (see duo_kv_pages_view)."""
+        v = L.duo_kv_pages_view_get(self.handle)
+        buf, base = self._page_state, self._page_state.data_ptr()
+
+        def view(ptr, n):
+            return buf[ptr - base:ptr - base + 4 * n].view(torch.int32)
+        return dict(table=view(v.table, self.B * v.max_pages).view(self.B, v.max_pages), held=view(v.held, self.B),
+                    refs=view(v.refs, self.num_pages), free_bits=view(v.free_bits, -(-self.num_pages // 32)))
+
+    def reserve(self, len_before, n_new=None, tokens=None):
+        """Rows for the next n_new (int32 [batch], default 1 each) tokens of
+        every sequence, behind its len_before (int32 [batch]; 0 starts a new
+        request): pages on a cache with ``manage_pages``, and the map of the
+        step's tokens in ``tokens`` (a TokenMap, returned); see
+        duo_kv_reserve.  Without ``tokens`` only the pages are reserved and
+        len_after (int32 [batch]) is returned."""
+        bp = _need(len_before, "len_before", torch.int32, (self.B,), self.device)
+        np_ = _need(n_new, "n_new", torch.int32, (self.B,), self.device) if n_new is not None else None
+        if tokens is None:
+            after = torch.empty(self.B, dtype=torch.int32, device=self.device)
+            with _on(self.device):
+                L.duo_kv_reserve(self.handle, bp, np_, 0, after.data_ptr(), None, None, None, None,
+                                 _stream(self.device))
+            return after
+        if tokens.batch != self.B or tokens.device != self.device:
+            raise ValueError("the token map is of another batch or device")
+        with _on(self.device):
+            L.duo_kv_reserve(self.handle, bp, np_, tokens.max_tokens, tokens.len_after.data_ptr(),
+                             tokens.cu.data_ptr(), tokens.seq.data_ptr(), tokens.pos.data_ptr(),
+                             tokens.slot.data_ptr(), _stream(self.device))
+        return tokens
 
     def fork(self, src: int, dst: int, length: int):
         """Sequence dst continues from the first ``length`` tokens of
@@ -231,6 +333,103 @@ class DuoKVCache:
         L.duo_decode_step(self.handle, layer, kp, vp, bp, qp, lp, float(scale), op, sp, self._ws.data_ptr(),
                           self._ws.numel(), _stream(self.device))
         return (out, lse) if lse is not None else out
+
+    def append_rope(self, layer: int, rope, q, k, v, len_before, tokens=None, n_new=None, out=None):
+        """Rotate queries and keys at their tokens' positions and append keys
+        and values, in one launch (duo_kv_append_rope).  q, k, v: bf16 rows of
+        the projections, token-major, strided or parts of one tensor.
+        tokens (a TokenMap): a ragged batch, q [T][Hq][d], k and v
+        [T][n_kv][d] with T = tokens.max_tokens.  Without it: a padded batch
+        [B][n][heads][d] and n_new int32 [B] (<= n).  len_before: int32 [B].
+        q may be None (keys and values only).  Returns the rotated queries
+        (contiguous, in ``out`` if given; rows without a token stay as they
+        were, zero where out is new)."""
+        if rope.d != self.d:
+            raise ValueError(f"rope of head_dim {rope.d}, expected {self.d}")
+        lead = (tokens.max_tokens,) if tokens is not None else tuple(k.shape[:2])
+        if tokens is None and (len(lead) != 2 or k.dim() != 4 or lead[0] != self.B):
+            raise ValueError(f"a padded batch is [{self.B}][tokens][heads][{self.d}]")
+        bp = _need(len_before, "len_before", torch.int32, (self.B,), self.device)
+        tmap = np_ = qr = op = None
+        if tokens is not None:
+            if n_new is not None:
+                raise ValueError("n_new belongs to a padded batch: the token map says how many tokens there are")
+            if tokens.batch != self.B or tokens.device != self.device:
+                raise ValueError("the token map is of another batch or device")
+            tmap = L.duo_token_map(tokens.seq.data_ptr(), tokens.pos.data_ptr(), tokens.slot.data_ptr(),
+                                   tokens.len_after.data_ptr())
+        elif n_new is not None:
+            np_ = _need(n_new, "n_new", torch.int32, (self.B,), self.device)
+        kr = _rows(k, "k", self.n_kv, self.d, lead, self.device)
+        vr = _rows(v, "v", self.n_kv, self.d, lead, self.device)
+        if q is not None:
+            qr = _rows(q, "q", self.hq, self.d, lead, self.device)
+            if out is None:
+                make = torch.empty if tokens is None and n_new is None else torch.zeros
+                out = make(*lead, self.hq, self.d, dtype=torch.bfloat16, device=self.device)
+            op = _need(out, "out", torch.bfloat16, (*lead, self.hq, self.d), self.device)
+        elif out is not None:
+            raise ValueError("out without q")
+        with _on(self.device):
+            L.duo_kv_append_rope(self.handle, layer, rope.handle, qr, kr, vr, bp, tmap, np_, lead[-1], op,
+                                 _stream(self.device))
+        return out
+
+    def step_rope(self, layer: int, rope, q, k, v, len_before, lengths, scale: float, out=None, lse=None,
+                  want_lse=False, q_rot=None):
+        """One decode step from the projections' rows (bf16 q [B][Hq][d], k and
+        v [B][n_kv][d], strided or parts of one tensor): rotate at positions
+        len_before, append, and decode over lengths (int32 [B], =
+        len_before + 1); see duo_decode_step_rope.  q_rot: bf16 [B][Hq][d]
+        scratch for the rotated queries (allocated if not given).  Returns
+        fp32 out [B][Hq][d] (and lse [B][Hq] if asked)."""
+        if rope.d != self.d:
+            raise ValueError(f"rope of head_dim {rope.d}, expected {self.d}")
+        qr = _rows(q, "q", self.hq, self.d, (self.B,), self.device)
+        kr = _rows(k, "k", self.n_kv, self.d, (self.B,), self.device)
+        vr = _rows(v, "v", self.n_kv, self.d, (self.B,), self.device)
+        bp = _need(len_before, "len_before", torch.int32, (self.B,), self.device)
+        lp = _need(lengths, "lengths", torch.int32, (self.B,), self.device)
+        if q_rot is None:
+            q_rot = torch.empty(self.B, self.hq, self.d, dtype=torch.bfloat16, device=self.device)
+        rp = _need(q_rot, "q_rot", torch.bfloat16, (self.B, self.hq, self.d), self.device)
+        if out is None:
+            out = torch.empty(self.B, self.hq, self.d, dtype=torch.float32, device=self.device)
+        op = _need(out, "out", torch.float32, (self.B, self.hq, self.d), self.device)
+        if want_lse and lse is None:
+            lse = torch.empty(self.B, self.hq, dtype=torch.float32, device=self.device)
+        sp = _need(lse, "lse", torch.float32, (self.B, self.hq), self.device) if lse is not None else None
+        with _on(self.device):
+            L.duo_decode_step_rope(self.handle, layer, rope.handle, qr, kr, vr, bp, lp, float(scale), rp, op, sp,
+                                   self._ws.data_ptr(), self._ws.numel(), _stream(self.device))
+        return (out, lse) if lse is not None else out
+
+    def prefill_rope(self, layer: int, rope, q, k, v, prefix_len, scale: float, n_new=None, out=None):
+        """A prompt chunk of one layer from the projections' rows (bf16 q
+        [B][C][Hq][d], k and v [B][C][n_kv][d], any strides with contiguous
+        heads): rotate at positions prefix_len + i and lay out head-major (one
+        launch), attend (``prefill``), then append the chunk, of which
+        sequence b has its first n_new[b] tokens (int32 [B], default C).
+        Returns fp32 out [B][Hq][C][d]; rows at and behind n_new[b] mean
+        nothing."""
+        if rope.d != self.d:
+            raise ValueError(f"rope of head_dim {rope.d}, expected {self.d}")
+        C = q.shape[1]
+        src = []
+        for t, name, heads in ((q, "q", self.hq), (k, "k", self.n_kv), (v, "v", self.n_kv)):
+            if t.dtype != torch.bfloat16:
+                raise TypeError(f"{name}: dtype {t.dtype}, expected {torch.bfloat16}")
+            if tuple(t.shape) != (self.B, C, heads, self.d):
+                raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(self.B, C, heads, self.d)}")
+            if t.device != self.device:
+                raise ValueError(f"{name}: on {t.device}, expected {self.device}")
+            src.append(t.transpose(1, 2))
+        dst = [torch.empty(t.shape, dtype=torch.bfloat16, device=self.device) for t in src]
+        rope.launch([(src[0], dst[0], True), (src[1], dst[1], True), (src[2], dst[2], False)], prefix_len)
+        with _on(self.device):
+            out = self.prefill(layer, *dst, prefix_len, scale, out=out)
+            self.append(layer, dst[1], dst[2], prefix_len, n_new)
+        return out
 
     def prefill(self, layer: int, q, k_chunk, v_chunk, prefix_len, scale: float, out=None):
         """q: bf16 [B][Hq][C][d]; k_chunk, v_chunk: bf16 [B][n_kv][C][d];

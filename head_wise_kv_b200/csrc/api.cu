@@ -8,7 +8,9 @@
 #include <algorithm>
 #include <new>
 
+#include "append_rope.cuh"
 #include "duo_internal.cuh"
+#include "pages.cuh"
 
 namespace {
 
@@ -93,6 +95,19 @@ size_t plan_layout(const duo_kv_desc* d, std::vector<duo::LayerLayout>* layers, 
 }
 
 int cuda_err(cudaError_t e) { return e == cudaSuccess ? DUO_OK : DUO_ERR_CUDA; }
+
+// Whether the handle's device is the current one.
+bool on_device(const duo_kv* kv) {
+    int dev = -1;
+    return cudaGetDevice(&dev) == cudaSuccess && dev == kv->device;
+}
+
+// Rows of a projection's output: present, aligned for 16-byte loads.
+int check_rows(const duo_rows* r) {
+    if (!r || !r->data) return DUO_ERR_INVALID_ARG;
+    if (!aligned16(r->data) || r->token_stride % 8 != 0 || r->head_stride % 8 != 0) return DUO_ERR_ALIGNMENT;
+    return DUO_OK;
+}
 
 }  // namespace
 
@@ -261,6 +276,75 @@ int duo_kv_append_rows(duo_kv* kv, int32_t layer, const uint16_t* k_new, const u
     return append_impl(kv, layer, k_new, v_new, len_before, n_new, n_new_max, r_pos_begin, r_pos_end, stream);
 }
 
+int duo_kv_append_rope(duo_kv* kv, int32_t layer, const duo_rope* rope, const duo_rows* q, const duo_rows* k,
+                       const duo_rows* v, const int32_t* len_before, const duo_token_map* map, const int32_t* n_new,
+                       int32_t n_tokens, uint16_t* q_out, duo_stream_t stream) {
+    if (!kv || layer < 0 || layer >= kv->desc.num_layers || !rope || n_tokens < 0) return DUO_ERR_INVALID_ARG;
+    if (rope->desc.head_dim != kv->desc.head_dim || (q != nullptr) != (q_out != nullptr)) return DUO_ERR_INVALID_ARG;
+    if (map && (n_new || !map->seq || !map->pos || !map->len_after)) return DUO_ERR_INVALID_ARG;
+    if (n_tokens == 0) return DUO_OK;
+    if (!len_before) return DUO_ERR_INVALID_ARG;
+    for (const duo_rows* r : {q, k, v}) {
+        if (r == q && !q) continue;
+        const int rc = check_rows(r);
+        if (rc) return rc;
+    }
+    for (const void* ptr : {static_cast<const void*>(len_before), static_cast<const void*>(n_new),
+                            static_cast<const void*>(map ? map->seq : nullptr),
+                            static_cast<const void*>(map ? map->pos : nullptr),
+                            static_cast<const void*>(map ? map->len_after : nullptr)})
+        if (reinterpret_cast<uintptr_t>(ptr) & 3) return DUO_ERR_ALIGNMENT;
+    if ((map && (reinterpret_cast<uintptr_t>(map->slot) & 7)) || !aligned16(q_out)) return DUO_ERR_ALIGNMENT;
+    if (!on_device(kv)) return DUO_ERR_INVALID_ARG;
+    const duo::LayerLayout& L = kv->layers[layer];
+    duo::AppendRopeParams p{};
+    if (q) p.in[0] = *q;
+    p.in[1] = *k;
+    p.in[2] = *v;
+    p.q_out = q_out;
+    p.len_before = len_before;
+    if (map) {
+        p.map_seq = map->seq;
+        p.map_pos = map->pos;
+        p.map_slot = map->slot;
+        p.len_after = map->len_after;
+    }
+    p.n_new = n_new;
+    p.n = n_tokens;
+    p.T = map ? int64_t(n_tokens) : int64_t(n_tokens) * kv->desc.batch;
+    p.kr = reinterpret_cast<uint16_t*>(kv->base + L.off_kr);
+    p.vr = reinterpret_cast<uint16_t*>(kv->base + L.off_vr);
+    p.ks = reinterpret_cast<uint16_t*>(kv->base + L.off_ks);
+    p.vs = reinterpret_cast<uint16_t*>(kv->base + L.off_vs);
+    p.pos = reinterpret_cast<int32_t*>(kv->base + L.off_pos);
+    p.status = kv->status;
+    p.cap = kv->desc.capacity;
+    p.B = kv->desc.batch;
+    p.hq = kv->desc.num_q_heads;
+    p.n_kv = kv->desc.num_kv_heads;
+    p.n_r = L.n_r;
+    p.n_s = L.n_s;
+    p.S = kv->desc.sink;
+    p.W = kv->desc.window;
+    p.fp8 = kv->fp8;
+    p.int4 = kv->int4;
+    memcpy(p.rank, L.rank, sizeof p.rank);
+    memcpy(p.is_r, L.is_r, sizeof p.is_r);
+    for (int g = 0; g < kv->desc.num_kv_heads; ++g) {
+        p.k_scale[g] = kv->k_scale[size_t(layer) * kv->desc.num_kv_heads + g];
+        p.v_scale[g] = kv->v_scale[size_t(layer) * kv->desc.num_kv_heads + g];
+    }
+    if (kv->page_tokens > 0) {
+        if (!kv->page_table && L.n_r > 0 && !(map && map->slot)) return DUO_ERR_INVALID_ARG;   // no page table set
+        p.page_tokens = kv->page_tokens;
+        p.num_pages = kv->num_pages;
+        p.max_pages = kv->max_pages;
+        p.page_table = kv->page_table;
+    }
+    p.table = duo::rope_table(rope);
+    return cuda_err(duo::launch_append_rope(p, kv->desc.head_dim, kv->num_sms, stream));
+}
+
 static int decode_slots(const duo_kv* kv) {
     const int ctas = kv->decode_ctas > 0 ? kv->decode_ctas
                                          : duo::decode_ctas_default(kv->num_sms, kv->desc.head_dim,
@@ -372,6 +456,25 @@ int duo_decode_step(duo_kv* kv, int32_t layer, const uint16_t* k_new, const uint
     rc = append_impl(kv, layer, k_new, v_new, len_before, nullptr, 1, nullptr, nullptr, stream);
     if (rc) return rc;
     if (kv->desc.head_dim == 128) p.len_before = len_before;   // read ahead of the append
+    const int G = kv->desc.num_q_heads / kv->desc.num_kv_heads;
+    return cuda_err(duo::launch_decode(p, kv->desc.head_dim, G, stream));
+}
+
+int duo_decode_step_rope(duo_kv* kv, int32_t layer, const duo_rope* rope, const duo_rows* q, const duo_rows* k,
+                         const duo_rows* v, const int32_t* len_before, const int32_t* len, float scale,
+                         uint16_t* q_rot, float* out, float* lse, void* workspace, size_t workspace_bytes,
+                         duo_stream_t stream) {
+    if (!len || !len_before || !q || !q_rot) return DUO_ERR_INVALID_ARG;
+    duo::DecodeParams p;
+    int rc = decode_setup(kv, layer, q_rot, len, nullptr, nullptr, nullptr, scale, out, lse, workspace,
+                          workspace_bytes, p);
+    if (rc) return rc;
+    rc = duo_kv_append_rope(kv, layer, rope, q, k, v, len_before, nullptr, nullptr, 1, q_rot, stream);
+    if (rc) return rc;
+    if (kv->desc.head_dim == 128) {
+        p.len_before = len_before;   // read ahead of the append
+        p.q_late = 1;
+    }
     const int G = kv->desc.num_q_heads / kv->desc.num_kv_heads;
     return cuda_err(duo::launch_decode(p, kv->desc.head_dim, G, stream));
 }
@@ -524,7 +627,79 @@ int duo_kv_set_page_table(duo_kv* kv, const int32_t* d_table, int32_t max_pages)
     if (reinterpret_cast<uintptr_t>(d_table) & 3) return DUO_ERR_ALIGNMENT;
     kv->page_table = d_table;
     kv->max_pages = max_pages;
+    kv->page_state = nullptr;
     return DUO_OK;
+}
+
+int duo_kv_pages_bytes(const duo_kv* kv, int32_t max_pages, size_t* bytes) {
+    if (!kv || !bytes || kv->page_tokens <= 0 || max_pages < 1) return DUO_ERR_INVALID_ARG;
+    if (kv->num_pages > 0x7fffffffLL - 32) return DUO_ERR_UNSUPPORTED;   // page numbers are int32
+    *bytes = duo::pages_layout(kv->desc.batch, max_pages, kv->num_pages, nullptr, nullptr);
+    return DUO_OK;
+}
+
+int duo_kv_pages_init(duo_kv* kv, int32_t max_pages, void* dev_buf, size_t buf_bytes, duo_stream_t stream) {
+    size_t need = 0;
+    const int rc = duo_kv_pages_bytes(kv, max_pages, &need);
+    if (rc) return rc;
+    if (!dev_buf) return DUO_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(dev_buf) % kAlign) return DUO_ERR_ALIGNMENT;
+    if (buf_bytes < need) return DUO_ERR_BUFFER_TOO_SMALL;
+    if (!on_device(kv)) return DUO_ERR_INVALID_ARG;
+    duo::PageState st;
+    duo::pages_layout(kv->desc.batch, max_pages, kv->num_pages, static_cast<char*>(dev_buf), &st);
+    const cudaError_t e = duo::launch_pages_init(st, kv->desc.batch, max_pages, kv->num_pages, stream);
+    if (e != cudaSuccess) return DUO_ERR_CUDA;
+    kv->page_table = st.table;
+    kv->max_pages = max_pages;
+    kv->page_state = static_cast<char*>(dev_buf);
+    return DUO_OK;
+}
+
+int duo_kv_pages_view_get(const duo_kv* kv, duo_kv_pages_view* out) {
+    if (!kv || !out || !kv->page_state) return DUO_ERR_INVALID_ARG;
+    duo::PageState st;
+    duo::pages_layout(kv->desc.batch, kv->max_pages, kv->num_pages, kv->page_state, &st);
+    out->table = st.table;
+    out->held = st.held;
+    out->refs = st.refs;
+    out->free_bits = st.free_bits;
+    out->max_pages = kv->max_pages;
+    return DUO_OK;
+}
+
+int duo_kv_reserve(duo_kv* kv, const int32_t* len_before, const int32_t* n_new, int32_t map_tokens,
+                   int32_t* len_after, int32_t* cu, int32_t* seq, int32_t* pos, int64_t* slot, duo_stream_t stream) {
+    if (!kv || !len_before || !len_after || map_tokens < 0) return DUO_ERR_INVALID_ARG;
+    // a map comes whole or not at all
+    const int given = (cu != nullptr) + (seq != nullptr) + (pos != nullptr) + (slot != nullptr);
+    if (given != 0 && given != 4) return DUO_ERR_INVALID_ARG;
+    if (given == 0 && map_tokens != 0) return DUO_ERR_INVALID_ARG;
+    if (kv->page_tokens > 0 && !kv->page_state) return DUO_ERR_INVALID_ARG;   // the caller keeps the table
+    for (const void* ptr : {static_cast<const void*>(len_before), static_cast<const void*>(n_new),
+                            static_cast<const void*>(len_after), static_cast<const void*>(cu),
+                            static_cast<const void*>(seq), static_cast<const void*>(pos)})
+        if (reinterpret_cast<uintptr_t>(ptr) & 3) return DUO_ERR_ALIGNMENT;
+    if (reinterpret_cast<uintptr_t>(slot) & 7) return DUO_ERR_ALIGNMENT;
+    if (!on_device(kv)) return DUO_ERR_INVALID_ARG;
+    duo::ReserveParams p{};
+    if (kv->page_tokens > 0)
+        duo::pages_layout(kv->desc.batch, kv->max_pages, kv->num_pages, kv->page_state, &p.st);
+    p.len_before = len_before;
+    p.n_new = n_new;
+    p.len_after = len_after;
+    p.cu = cu;
+    p.seq = seq;
+    p.pos = pos;
+    p.slot = slot;
+    p.status = kv->status;
+    p.cap = kv->desc.capacity;
+    p.num_pages = int32_t(kv->num_pages);
+    p.page_tokens = kv->page_tokens;
+    p.max_pages = kv->max_pages;
+    p.B = kv->desc.batch;
+    p.T = map_tokens;
+    return cuda_err(duo::launch_reserve(p, stream));
 }
 
 int duo_kv_fork(duo_kv* kv, int32_t src, int32_t dst, int32_t len, duo_stream_t stream) {
@@ -534,6 +709,20 @@ int duo_kv_fork(duo_kv* kv, int32_t src, int32_t dst, int32_t len, duo_stream_t 
     const bool paged = kv->page_tokens > 0;
     const int units = paged ? (len + kv->page_tokens - 1) / kv->page_tokens : 1;
     if (paged && len > 0 && (!kv->page_table || units > kv->max_pages)) return DUO_ERR_INVALID_ARG;
+    if (kv->page_state) {   // the library's table: dst shares the full pages and gets one for a partly filled last one
+        if (!on_device(kv)) return DUO_ERR_INVALID_ARG;
+        duo::ShareParams s{};
+        duo::pages_layout(kv->desc.batch, kv->max_pages, kv->num_pages, kv->page_state, &s.st);
+        s.status = kv->status;
+        s.num_pages = int32_t(kv->num_pages);
+        s.max_pages = kv->max_pages;
+        s.page_tokens = kv->page_tokens;
+        s.src = src;
+        s.dst = dst;
+        s.len = len;
+        const int rc = cuda_err(duo::launch_share(s, static_cast<cudaStream_t>(stream)));
+        if (rc) return rc;
+    }
     for (int l = 0; l < kv->desc.num_layers; ++l) {
         const duo::LayerLayout& L = kv->layers[l];
         duo::ForkParams p{};

@@ -452,7 +452,7 @@ __global__ void __launch_bounds__(I4 ? kThreadsI4 : kThreads, 1)
     // be stale (the last row of a retrieval segment, one slot of a streaming
     // ring): the lengths, q and every other tile are read at once, and a
     // producer waits for the append before the first tile that may hold such
-    // a row.  Any sequence whose length does not grow by exactly one turns
+    // a row, as the q warp does for queries that the append rotates (q_late).  Any sequence whose length does not grow by exactly one turns
     // this off for the launch.
     const bool step_mode = p.len_before != nullptr;
     if (!step_mode) asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -553,6 +553,8 @@ __global__ void __launch_bounds__(I4 ? kThreadsI4 : kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_addr(&pg_ready));
             }
+            // the step's append writes the rotated queries as well
+            if (early && p.q_late) asm volatile("griddepcontrol.wait;" ::: "memory");
             // Runs up to two pieces ahead of the S products (two q buffers).
             int pi = 0;
             for (int64_t gb = gb_begin; gb < gb_end; ++pi) {

@@ -47,6 +47,7 @@ struct duo_kv {
     int64_t num_pages = 0;
     const int32_t* page_table = nullptr;    // device [B][max_pages], caller-owned
     int max_pages = 0;
+    char* page_state = nullptr;             // device, caller-owned: the table is the library's (pages.cu)
     std::vector<float> k_scale, v_scale;    // [L][n_kv] (FP8)
     std::vector<duo::DecodeMaps> maps;      // per layer (head_dim 128 only)
 };
@@ -94,6 +95,7 @@ struct DecodeParams {
     // tensor-core kernel, step mode (duo_decode_step): lengths before the
     // append that precedes this launch in the stream (null otherwise)
     const int32_t* len_before;
+    int q_late;                  // step mode: that append writes q too (duo_decode_step_rope)
 };
 
 struct AppendParams {

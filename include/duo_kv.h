@@ -26,8 +26,10 @@
  *   - Sequence lengths live on the device and are passed on every call; the
  *     library keeps no per-sequence state besides the cache contents.
  *   - q and K are already position-encoded (e.g. RoPE) by the caller, each
- *     at the token's original position; the library applies no positional
- *     encoding.  Ring slots keep each token's original position.
+ *     at the token's original position, in every call whose name does not
+ *     say "rope"; duo_rope_apply, duo_kv_append_rope and
+ *     duo_decode_step_rope rotate them.  Ring slots keep each token's
+ *     original position.
  *   - Return value: DUO_OK (0) or a negative DUO_ERR_* code.  On an error
  *     nothing was launched.  Errors found by kernels (a length beyond the
  *     capacity, an empty sequence, a pipeline wait that timed out) set bits
@@ -406,8 +408,9 @@ DUO_API int duo_kv_check_wait_timeout(duo_kv* kv, uint64_t limit_ns, duo_stream_
  * the same index in every layer's pool) holding positions
  * i*page_tokens .. (i+1)*page_tokens - 1 of sequence b, or -1 for none.
  * The table stays the caller's; the library reads it in later calls
- * (stream-ordered), so the caller updates it as sequences grow.  Host only;
- * INVALID_ARG on a contiguous cache or max_pages < 1. */
+ * (stream-ordered), so the caller updates it as sequences grow (or has the
+ * library keep it: duo_kv_pages_init, whose table this call takes out of
+ * use).  Host only; INVALID_ARG on a contiguous cache or max_pages < 1. */
 DUO_API int duo_kv_set_page_table(duo_kv* kv, const int32_t* d_table, int32_t max_pages);
 
 /* Prefix sharing: make sequence dst continue from the first len tokens of
@@ -421,7 +424,10 @@ DUO_API int duo_kv_set_page_table(duo_kv* kv, const int32_t* d_table, int32_t ma
  * heads of a contiguous cache copy rows [0, len).  Paged caches: the caller
  * first sets dst's page-table entries for the prefix's pages; an entry equal
  * to src's shares that pool page (nothing is copied), any other page
- * receives a copy of src's rows.  The page holding the last, partly filled
+ * receives a copy of src's rows.  Where the library keeps the table
+ * (duo_kv_pages_init) it sets those entries itself: dst gives its pages
+ * back, shares src's full pages and gets the lowest free page for a partly
+ * filled last one.  The page holding the last, partly filled
  * block of the prefix (len not a multiple of page_tokens) must differ
  * between the two (DUO_STATUS_SHARED_PAGE otherwise); shared pages must not
  * be written through either sequence afterwards (they hold positions < len,
@@ -430,6 +436,221 @@ DUO_API int duo_kv_set_page_table(duo_kv* kv, const int32_t* d_table, int32_t ma
  * position len - 1 (src holds a different number of tokens).  One launch per
  * layer on `stream`, ordered like appends. */
 DUO_API int duo_kv_fork(duo_kv* kv, int32_t src, int32_t dst, int32_t len, duo_stream_t stream);
+
+/* ------------------------------------------------------ rotary positions */
+
+/* Which elements of a head form the pairs that turn together. */
+enum {
+    DUO_ROPE_HALF = 0,          /* i and i + rot_dim / 2                       */
+    DUO_ROPE_INTERLEAVED = 1    /* 2i and 2i + 1                               */
+};
+
+/* How the angles per position f_i = theta^(-2i / rot_dim), i < rot_dim / 2,
+ * are changed for contexts longer than the one trained on (s = factor,
+ * L = original_len; L * f / 2 pi is the number of turns a pair makes in L
+ * positions):
+ *   NONE     f
+ *   LINEAR   f / s
+ *   NTK      f with theta * s^(rot_dim / (rot_dim - 2)): the slowest pair is
+ *            stretched by s, the fastest keeps its angle
+ *   YARN     f (1 - r_i) + (f / s) r_i, r_i the ramp from 0 at pair
+ *            floor(c(high)) to 1 at pair ceil(c(low)), both kept in
+ *            [0, rot_dim - 1], where c(t) = rot_dim ln(L / (2 pi t)) / (2 ln
+ *            theta) is the pair that makes t turns over L (low = 1 and
+ *            high = 32 if given as 0).  Cosine and sine are multiplied by
+ *            0.1 ln(s) + 1 for s > 1 unless magnitude says otherwise
+ *   BANDS    (f / s) (1 - r) + f r with r = clamp((L f / 2 pi - low) /
+ *            (high - low), 0, 1) (low = 1 and high = 4 if given as 0)
+ *   FACTORS  f / pair_factors[i] (HOST array [rot_dim / 2], copied) */
+enum {
+    DUO_ROPE_NONE = 0, DUO_ROPE_LINEAR = 1, DUO_ROPE_NTK = 2,
+    DUO_ROPE_YARN = 3, DUO_ROPE_BANDS = 4, DUO_ROPE_FACTORS = 5
+};
+
+/* Element types of duo_rope_apply. */
+enum { DUO_BF16 = 0, DUO_FP16 = 1, DUO_FP32 = 2 };
+
+/* head_dim 64 or 128; rot_dim a multiple of 16, at most head_dim (the
+ * elements behind the first rot_dim pass through); theta > 1; factor >= 1
+ * and original_len > 0 where the scaling uses them; magnitude: what cosine
+ * and sine are multiplied by, 0 = the scaling's own (1 except for YARN). */
+typedef struct {
+    int32_t head_dim;
+    int32_t rot_dim;
+    int32_t layout;
+    int32_t scaling;
+    double theta;
+    double factor;
+    double original_len;
+    double low;
+    double high;
+    double magnitude;
+    const double* pair_factors;
+} duo_rope_desc;
+
+/* Opaque host-side plan: the angles, ready for kernels (host memory only). */
+typedef struct duo_rope duo_rope;
+
+/* Check *desc and make a plan.  Errors: INVALID_ARG, UNSUPPORTED (head_dim,
+ * rot_dim). */
+DUO_API int duo_rope_create(const duo_rope_desc* desc, duo_rope** out);
+
+/* Release a plan.  NULL is a no-op. */
+DUO_API int duo_rope_free(duo_rope* rope);
+
+/* The plan's angles per position (radians, [rot_dim / 2]) and magnitude. */
+DUO_API int duo_rope_frequencies(const duo_rope* rope, double* angle, double* magnitude);
+
+/* One tensor of duo_rope_apply: [batch][heads][n][head_dim] by strides in
+ * elements (batch, head, token; the head_dim elements are contiguous).
+ * Every stride and both pointers are multiples of 16 bytes.  rotate = 0
+ * copies the tensor into its new layout (values next to queries and keys).
+ * out may be in (with the same strides); otherwise the two do not overlap,
+ * and the elements of out are distinct. */
+typedef struct {
+    const void* in;
+    void* out;
+    int32_t heads;
+    int32_t rotate;
+    int64_t in_stride[3];
+    int64_t out_stride[3];
+} duo_rope_tensor;
+
+/* Rotate up to three tensors of one batch in one launch (queries, keys, and
+ * values laid out beside them).  Pair (x0, x1) number i of a head at
+ * position p becomes, with a = p f_i and m the magnitude,
+ *   y0 = m (x0 cos a - x1 sin a),  y1 = m (x1 cos a + x0 sin a);
+ * transpose != 0 turns the other way (sin a with the other sign): the
+ * transposed map, which takes the gradient of y to the gradient of x.
+ *   dtype: DUO_BF16, DUO_FP16 or DUO_FP32, of every tensor;
+ *   positions: device int32, any sign: per_token == 0: [batch], token i of
+ *     sequence b at positions[b] + i; else [batch][n];
+ *   n_new: device int32 [batch] or NULL: only the first n_new[b] tokens of a
+ *     sequence are read and written, the rest of out stays as it was.
+ * Arithmetic is fp32, rounded once; angles are exact multiples of a turn in
+ * 64-bit fixed point, so far positions lose nothing.  Runs on the current
+ * device, which holds every tensor. */
+DUO_API int duo_rope_apply(const duo_rope* rope, int32_t dtype, int32_t transpose, int32_t batch, int32_t n,
+                           const duo_rope_tensor* tensors, int32_t num_tensors, const int32_t* positions,
+                           int32_t per_token, const int32_t* n_new, duo_stream_t stream);
+
+/* Rows of a projection's output, token-major: element (token t, head h, i)
+ * at data[t * token_stride + h * head_stride + i], bf16.  data and both
+ * strides are multiples of 16 bytes (8 elements).  q, k and v may be parts
+ * of one tensor. */
+typedef struct {
+    const uint16_t* data;
+    int64_t token_stride;
+    int64_t head_stride;
+} duo_rows;
+
+/* A ragged batch of tokens, one entry per row, as duo_kv_reserve writes it
+ * (device arrays): the sequence (-1: no token, its row is skipped), its
+ * position, and its row in the retrieval pool, page * page_tokens + offset
+ * (-1: no page); slot may be NULL for contiguous caches (row = position)
+ * and is read through the page table where it is NULL for paged ones.
+ * len_after: [batch], every sequence's tokens after this step.  A token
+ * appears once. */
+typedef struct {
+    const int32_t* seq;
+    const int32_t* pos;
+    const int64_t* slot;
+    const int32_t* len_after;
+} duo_token_map;
+
+/* Rotary positions and the append of one layer in one launch: queries are
+ * rotated into q_out, keys are rotated and written to the caches as
+ * duo_kv_append writes them, values are written as given; positions, rings,
+ * quantisation (from the fp32 rotated value, rounded once) and status bits
+ * as there.
+ *   q, k, v: rows of num_q_heads, num_kv_heads and num_kv_heads heads (q may
+ *     be NULL with q_out NULL: keys and values only);
+ *   len_before: device int32 [batch], tokens held before the step;
+ *   map != NULL: n_tokens rows, row t is the map's token t; n_new NULL; the
+ *     tokens of a sequence are those at len_before[b] .. len_after[b] - 1;
+ *   map == NULL: a padded batch of n_tokens rows per sequence, row
+ *     b * n_tokens + i holds token i of sequence b, at position
+ *     len_before[b] + i; n_new: device int32 [batch] (<= n_tokens) or NULL =
+ *     n_tokens for every sequence;
+ *   q_out: [rows][num_q_heads][d] bf16, contiguous; rows without a token stay
+ *     as they were.
+ * rope's head_dim is the cache's.  The cache's device must be the current
+ * one (else INVALID_ARG).  A map entry out of range is skipped and sets
+ * DUO_STATUS_BAD_LENGTH (sequence, position), OVER_CAPACITY or NO_PAGE. */
+DUO_API int duo_kv_append_rope(duo_kv* kv, int32_t layer, const duo_rope* rope, const duo_rows* q,
+                               const duo_rows* k, const duo_rows* v, const int32_t* len_before,
+                               const duo_token_map* map, const int32_t* n_new, int32_t n_tokens, uint16_t* q_out,
+                               duo_stream_t stream);
+
+/* One decode step of one layer from the projections' outputs: the result is
+ * that of duo_kv_append_rope (padded, one token per sequence) into q_rot
+ * ([batch][num_q_heads][d] bf16, caller's scratch), then duo_decode_attn on
+ * q_rot.  As in duo_decode_step the attention kernel reads ahead of the
+ * append (head_dim 128, len[b] = len_before[b] + 1 for every sequence); it
+ * waits for the rotated queries before its first product. */
+DUO_API int duo_decode_step_rope(duo_kv* kv, int32_t layer, const duo_rope* rope, const duo_rows* q,
+                                 const duo_rows* k, const duo_rows* v, const int32_t* len_before,
+                                 const int32_t* len, float scale, uint16_t* q_rot, float* out, float* lse,
+                                 void* workspace, size_t workspace_bytes, duo_stream_t stream);
+
+/* --------------------------------------- block tables and slot maps on the GPU */
+
+/* Device views of a page state (duo_kv_pages_init), for verification and
+ * checkpoints: the page table of duo_kv_set_page_table [batch][max_pages],
+ * pages held by each sequence [batch], sequences holding each page
+ * [num_pages], and one bit per page that none holds
+ * [ceil(num_pages / 32)], page p at bit p mod 32 of word p / 32. */
+typedef struct {
+    int32_t* table;
+    int32_t* held;
+    int32_t* refs;
+    uint32_t* free_bits;
+    int32_t max_pages;
+} duo_kv_pages_view;
+
+/* Bytes of device memory the page state of this paged cache needs. */
+DUO_API int duo_kv_pages_bytes(const duo_kv* kv, int32_t max_pages, size_t* bytes);
+
+/* Let the library keep a paged cache's page table: lay the state out in
+ * dev_buf (caller-allocated, 256-byte aligned, on the cache's device), with
+ * every page free, and use its table from now on (until
+ * duo_kv_set_page_table sets another).  duo_kv_reserve then hands pages out
+ * and duo_kv_fork shares them.  INVALID_ARG on a contiguous cache. */
+DUO_API int duo_kv_pages_init(duo_kv* kv, int32_t max_pages, void* dev_buf, size_t buf_bytes, duo_stream_t stream);
+
+/* The views of the state; INVALID_ARG where the library keeps none. */
+DUO_API int duo_kv_pages_view_get(const duo_kv* kv, duo_kv_pages_view* out);
+
+/* Reserve rows for the next tokens of every sequence and map each token to
+ * its sequence, position and row: once per step, for all layers.
+ *   len_before: device int32 [batch], tokens each sequence holds; 0 starts a
+ *     new request in the slot;
+ *   n_new: device int32 [batch], tokens to come, or NULL = 1 each;
+ *   map_tokens: entries of seq, pos and slot (0 with all three and cu NULL:
+ *     no map);
+ *   len_after: [batch] = len_before + n_new where served, else len_before;
+ *   cu: [batch + 1], tokens served before each sequence: sequence b's are
+ *     entries cu[b] .. cu[b + 1] - 1 of the map, in position order;
+ *   seq, pos (int32), slot (int64): [map_tokens] as in duo_token_map,
+ *     entries behind cu[batch] are -1.
+ * Paged caches (with duo_kv_pages_init): first every sequence gives back the
+ * pages that hold none of its len_before tokens (a page that a fork shares
+ * stays until its last holder leaves), then sequences in order get the
+ * pages their new tokens lack, the lowest free ones first.  A sequence that
+ * needs pages is served as long as the needs up to and including its own,
+ * those of refused ones too, do not exceed the free pages; one that needs
+ * none is served whatever the others need.  Refused: no pages
+ * (DUO_STATUS_NO_PAGE); beyond capacity or max_pages, or a map that is too
+ * small for the tokens asked for up to and including its own
+ * (OVER_CAPACITY); a partly filled last page that another sequence shares
+ * (SHARED_PAGE).  Negative lengths, and len_before beyond capacity
+ * (BAD_LENGTH), leave the sequence as it is.  Nothing is read back: the call
+ * can be captured, and the table is the same for the same calls.
+ * Contiguous caches: slot = b * capacity + position, no state.  Calls are
+ * ordered like appends.  The cache's device must be the current one. */
+DUO_API int duo_kv_reserve(duo_kv* kv, const int32_t* len_before, const int32_t* n_new, int32_t map_tokens,
+                           int32_t* len_after, int32_t* cu, int32_t* seq, int32_t* pos, int64_t* slot,
+                           duo_stream_t stream);
 
 /* Override the number of CTAs the decode kernel splits the keys over
  * (0 = one persistent wave, the default).  For tests of split invariance;

@@ -400,3 +400,136 @@ def quantize_kv_int4(x, scale: float) -> np.ndarray:
 def dequantize_kv_int4(packed, scale: float) -> np.ndarray:
     """Values packed INT4 cache bytes stand for: scale * code, float64 (exact)."""
     return float(np.float32(scale)) * int4_unpack(packed).astype(np.float64)
+
+
+# ------------------------------------------------------------- rotary positions
+def rope_frequencies(rot_dim, theta=10000.0, scaling="none", factor=1.0, original_len=0.0, low=0.0, high=0.0,
+                     pair_factors=None):
+    """(angle per position of each pair, magnitude), float64: theta^(-2i / rot_dim)
+    changed as the scaling says (see duo_kv.h, "rotary positions")."""
+    i = np.arange(rot_dim // 2, dtype=np.float64)
+    base = theta * factor ** (rot_dim / (rot_dim - 2.0)) if scaling == "ntk" else theta
+    f = base ** (-2.0 * i / rot_dim)
+    turns = original_len * f / (2 * np.pi)          # over the original length
+    if scaling == "linear":
+        return f / factor, 1.0
+    if scaling == "bands":
+        lo, hi = low or 1.0, high or 4.0
+        keep = np.clip((turns - lo) / (hi - lo), 0, 1)
+        return keep * f + (1 - keep) * f / factor, 1.0
+    if scaling == "yarn":
+        slow, fast = low or 1.0, high or 32.0
+
+        def pair_with(t):
+            return rot_dim * np.log(original_len / (2 * np.pi * t)) / (2 * np.log(theta))
+        first, last = max(np.floor(pair_with(fast)), 0.0), min(np.ceil(pair_with(slow)), rot_dim - 1.0)
+        stretch = np.clip((i - first) / max(last - first, 1e-3), 0, 1)
+        return (1 - stretch) * f + stretch * f / factor, 0.1 * np.log(factor) + 1.0 if factor > 1 else 1.0
+    if scaling == "factors":
+        return f / np.asarray(pair_factors, dtype=np.float64), 1.0
+    return f, 1.0
+
+
+def rope_rotate(x, positions, freq, magnitude=1.0, layout="half", transpose=False):
+    """x float64 [..., n, d], positions [n] or broadcastable to x's leading
+    shape: every pair times magnitude * exp(+-i p f), the rest as it is."""
+    x = np.asarray(x, dtype=np.float64)
+    rot = 2 * len(freq)
+    angle = np.asarray(positions, dtype=np.float64)[..., None] * freq
+    z = magnitude * np.exp((-1j if transpose else 1j) * angle)
+    y = x.copy()
+    a, b = (slice(0, rot // 2), slice(rot // 2, rot)) if layout == "half" else (slice(0, rot, 2), slice(1, rot, 2))
+    w = (x[..., a] + 1j * x[..., b]) * z
+    y[..., a], y[..., b] = w.real, w.imag
+    return y
+
+
+# ------------------------------------------------------- block tables and slot maps
+class PageTables:
+    """Block tables kept page by page: the plain form of duo_kv_reserve and of
+    duo_kv_fork's sharing, one sequence, page and token after another."""
+
+    def __init__(self, batch, num_pages, page_tokens, max_pages, capacity):
+        self.B, self.N, self.pt, self.most, self.cap = batch, num_pages, page_tokens, max_pages, capacity
+        self.pages = [[] for _ in range(batch)]      # of each sequence, in order
+        self.refs = [0] * num_pages
+
+    def _give_back(self, b, keep):
+        while len(self.pages[b]) > keep:
+            self.refs[self.pages[b].pop()] -= 1
+
+    def _lowest(self, n):
+        free = [p for p in range(self.N) if self.refs[p] == 0][:n] if n else []
+        for p in free:
+            self.refs[p] = 1
+        return free
+
+    def _cover(self, tokens):
+        return -(-tokens // self.pt)
+
+    def reserve(self, before, new, map_tokens=None):
+        """Returns (len_after, cu, seq, pos, slot, refused) with refused the
+        set of reasons: "length", "capacity", "page", "shared", "map"."""
+        refused = set()
+        sane = [0 <= lb <= self.cap and n >= 0 for lb, n in zip(before, new)]
+        for b in range(self.B):
+            if sane[b]:
+                self._give_back(b, self._cover(before[b]))
+        free = sum(r == 0 for r in self.refs)
+        asked_pages = asked_tokens = 0
+        grants = []
+        for b, (lb, n) in enumerate(zip(before, new)):
+            if not sane[b]:
+                refused.add("length")
+                grants.append(None)
+                continue
+            total = self._cover(lb + n)
+            if lb + n > self.cap or total > self.most:
+                refused.add("capacity")
+                grants.append(None)
+                continue
+            have = len(self.pages[b])
+            if n > 0 and lb % self.pt and have == self._cover(lb) and self.refs[self.pages[b][-1]] > 1:
+                refused.add("shared")
+                grants.append(None)
+                continue
+            need = max(total - have, 0)
+            asked_pages += need
+            asked_tokens += n
+            if need > 0 and asked_pages > free:
+                refused.add("page")
+            if map_tokens is not None and asked_tokens > map_tokens:
+                refused.add("map")
+            ok = not (need > 0 and asked_pages > free) and not (map_tokens is not None and asked_tokens > map_tokens)
+            grants.append(need if ok else None)
+        after, cu, seq, pos, slot = [], [0], [], [], []
+        for b, (lb, n) in enumerate(zip(before, new)):
+            if grants[b] is not None:
+                self.pages[b] += self._lowest(grants[b])
+                for p in range(lb, lb + n):
+                    seq.append(b)
+                    pos.append(p)
+                    slot.append(self.pages[b][p // self.pt] * self.pt + p % self.pt)
+            after.append(lb + n if grants[b] is not None else lb)
+            cu.append(len(seq))
+        if map_tokens is not None:
+            for x in (seq, pos, slot):
+                x += [-1] * (map_tokens - len(x))
+        return after, cu, seq, pos, slot, refused
+
+    def fork(self, src, dst, length):
+        """True where src holds the prefix and dst got a page for its end."""
+        full, partly = length // self.pt, length % self.pt > 0
+        enough = len(self.pages[src]) >= full + partly
+        self._give_back(dst, 0)
+        if not enough:
+            return False
+        self.pages[dst] = self.pages[src][:full]
+        for p in self.pages[dst]:
+            self.refs[p] += 1
+        last = self._lowest(1) if partly else []
+        self.pages[dst] = self.pages[dst] + last
+        return not partly or len(last) == 1
+
+    def table(self):
+        return np.array([p + [-1] * (self.most - len(p)) for p in self.pages], dtype=np.int32)

@@ -1,0 +1,385 @@
+"""Rotary append and decode step (duo_kv_append_rope, duo_decode_step_rope,
+prefill_rope) on the GPU.
+
+Each append runs on twin caches: one with append_rope, one with the oracle's
+rotation worked out in fp64, rounded to bf16 and appended with duo_kv_append.
+Values, positions and every row that a step must not touch have to be the
+same bytes.  Keys and rotated queries are compared with the fp64 rotation:
+fp32 arithmetic (2^-20 of the pair's magnitudes, see test_gpu_rope.py) and
+one rounding: half a step of bf16 (2^-8), of E4M3 (2^-4 of the value, at
+least half the smallest step 2^-10, times the scale) or of INT4 (half a code
+times the scale).
+"""
+import numpy as np
+import pytest
+import torch
+
+from _harness import assert_close
+from oracle import duo_oracle as O
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda", 0)
+PAGE = 256
+KINDS = ["bf16", "fp8", "int4", "paged_bf16", "paged_fp8", "paged_int4"]
+SCALING = dict(scaling="bands", factor=8.0, original_len=2048)
+
+
+class Setup:
+    def __init__(self, kind, B=3, hq=8, n_kv=4, d=128, sink=4, window=33, cap=1500, rot=None, layout="half", caches=2,
+                 mask=None, num_pages=None):
+        from head_wise_kv_b200 import DuoKVCache, Rope
+        self.kv = kind.replace("paged_", "")
+        self.B, self.hq, self.n_kv, self.d, self.S, self.W = B, hq, n_kv, d, sink, window
+        self.mask = np.array([g % 2 == 0 for g in range(n_kv)] if mask is None else mask, dtype=np.uint8)
+        rng = np.random.default_rng(7)
+        self.ks, self.vs = (rng.uniform(0.3, 0.6, (1, n_kv)).astype(np.float32) for _ in range(2))
+        if self.kv == "bf16":
+            self.ks = self.vs = np.ones((1, n_kv), dtype=np.float32)
+        paged = kind.startswith("paged")
+        per = -(-cap // PAGE)
+        kw = dict(page_tokens=PAGE, num_pages=num_pages or B * per + 2) if paged else {}
+        quant = {} if self.kv == "bf16" else dict(k_scale=self.ks, v_scale=self.vs)
+        self.caches = [DuoKVCache(1, B, hq, n_kv, d, sink, window, cap, self.mask[None], device=DEV, kv_dtype=self.kv,
+                                  **quant, **kw) for _ in range(caches)]
+        for c in self.caches[1:]:
+            c.buf.copy_(self.caches[0].buf)
+        if paged:
+            perm = rng.permutation(kw["num_pages"])[:B * per].reshape(B, per).astype(np.int32)
+            for c in self.caches:
+                c.set_page_table(torch.from_numpy(perm).to(DEV))
+        self.rope = Rope(d, rot_dim=rot, layout=layout, **SCALING)
+        self.freq, self.mag = O.rope_frequencies(rot or d, **SCALING)
+        self.layout, self.rot = layout, rot or d
+
+    def rotate(self, x, pos):
+        """x [..., d] tensor, pos broadcast against x's leading shape."""
+        x64 = x.double().cpu().numpy()
+        return O.rope_rotate(x64, np.asarray(pos), self.freq, self.mag, self.layout)
+
+    def slack(self, x):
+        x64 = np.abs(x.double().cpu().numpy())
+        pair = np.zeros_like(x64)
+        a, b = (slice(0, self.rot // 2), slice(self.rot // 2, self.rot)) if self.layout == "half" else \
+            (slice(0, self.rot, 2), slice(1, self.rot, 2))
+        pair[..., a] = pair[..., b] = x64[..., a] + x64[..., b]
+        return self.mag * pair * 2.0 ** -20
+
+    def key_rounding(self, ref, g):
+        s = float(self.ks[0, g])
+        if self.kv == "bf16":
+            return np.abs(ref) * 2.0 ** -8
+        if self.kv == "fp8":
+            return np.maximum(np.abs(ref) * 2.0 ** -4, s * 2.0 ** -10)
+        return np.full(ref.shape, s / 2)
+
+    def values(self, codes, g, ks=True):
+        """Rows of a cache region as the values they stand for."""
+        s = float((self.ks if ks else self.vs)[0, g])
+        if self.kv == "bf16":
+            return codes.double().cpu().numpy()
+        c = codes.cpu().numpy()
+        return O.dequantize_kv(c, s) if self.kv == "fp8" else O.dequantize_kv_int4(c, s)
+
+
+def _qkv(st, T, seed, lead=None):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(*(lead or (T,)), st.hq + 2 * st.n_kv, st.d, generator=g).to(torch.bfloat16).to(DEV)
+    return x.split([st.hq, st.n_kv, st.n_kv], -2)
+
+
+def _twin_append(st, cache, k, v, before, counts, n):
+    """The same tokens through duo_kv_append: k, v [B][n][n_kv][d]."""
+    pos = np.asarray(before)[:, None, None] + np.arange(n)[None, :, None]
+    kr = torch.from_numpy(st.rotate(k, pos)).to(torch.bfloat16).to(DEV)
+    cache.append(0, kr.transpose(1, 2).contiguous(), v.transpose(1, 2).contiguous(),
+                 torch.tensor(before, dtype=torch.int32, device=DEV), torch.tensor(counts, dtype=torch.int32, device=DEV))
+
+
+def _same(a, b):
+    """The same bytes (rows never written may hold NaN patterns)."""
+    return torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
+
+
+def _compare(st, k, before, counts):
+    """caches[0] (append_rope) against caches[1] and the fp64 keys of this step."""
+    a, b = (c.layer_views(0) for c in st.caches)
+    assert st.caches[0].status() == st.caches[1].status() == 0
+    for name in ("v_retrieval", "v_streaming", "positions"):
+        assert _same(a[name], b[name]), name
+    table = st.caches[0]._page_table
+    seen = {n: torch.zeros(a[n].shape[:-1], dtype=torch.bool) for n in ("k_retrieval", "k_streaming")}
+    for s, (lb, n) in enumerate(zip(before, counts)):
+        for i in range(n):
+            p = lb + i
+            for g in range(st.n_kv):
+                r = a["head_rank"][g]
+                if st.mask[g]:
+                    at = (int(table[s, p // PAGE]), r, p % PAGE) if table is not None else (s, r, p)
+                    name = "k_retrieval"
+                elif p < st.S or p >= lb + n - st.W:
+                    at, name = (s, r, p if p < st.S else st.S + (p - st.S) % st.W), "k_streaming"
+                else:
+                    continue
+                seen[name][at] = True
+                if i % 7 == 0 or i >= n - 3:
+                    ref = st.rotate(k[s, i, g], p)
+                    err = np.abs(st.values(a[name][at], g) - ref)
+                    if st.kv == "int4":
+                        sc = float(st.ks[0, g])
+                        ref = np.clip(ref, -8 * sc, 7 * sc)
+                        err = np.abs(st.values(a[name][at], g) - ref)
+                    assert np.all(err <= st.key_rounding(ref, g) * (1 + 2.0 ** -10) + st.slack(k[s, i, g])), (s, p, g)
+    for name, m in seen.items():     # what the step does not write stays as it was
+        assert _same(a[name][~m.to(DEV)], b[name][~m.to(DEV)]), name
+        b[name].copy_(a[name])       # later steps start from the same bytes
+
+
+@pytest.mark.parametrize("kind,layout,rot,d", [(kind, layout, rot, 128) for kind in KINDS for layout, rot in
+                                               (("half", None), ("interleaved", 64))] + [("bf16", "half", 32, 64)])
+def test_padded(kind, layout, rot, d):
+    st = Setup(kind, d=d, rot=rot, layout=layout)
+    lens = [0, 0, 0]
+    for step, (n, counts) in enumerate([(70, [70, 1, 0]), (1, [1, 1, 1]), (300, [300, 255, 33]), (5, [0, 5, 2]),
+                                        (37, [37, 36, 35])]):
+        q, k, v = _qkv(st, 0, step, (st.B, n))
+        out = torch.full((st.B, n, st.hq, st.d), 3.0, dtype=torch.bfloat16, device=DEV)
+        bt = torch.tensor(lens, dtype=torch.int32, device=DEV)
+        even = len(set(counts)) == 1 and counts[0] == n
+        st.caches[0].append_rope(0, st.rope, q, k, v, bt, out=out,
+                                 n_new=None if even else torch.tensor(counts, dtype=torch.int32, device=DEV))
+        _twin_append(st, st.caches[1], k, v, lens, counts, n)
+        for b, c in enumerate(counts):
+            assert (out[b, c:] == 3).all()
+            ref = st.rotate(q[b, :c], lens[b] + np.arange(c)[:, None])
+            err = np.abs(out[b, :c].double().cpu().numpy() - ref)
+            assert np.all(err <= np.abs(ref) * 2.0 ** -8 * (1 + 2.0 ** -10) + st.slack(q[b, :c]))
+        _compare(st, k, lens, counts)
+        lens = [a + b for a, b in zip(lens, counts)]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "paged_fp8"])
+@pytest.mark.parametrize("with_slot", [True, False])
+def test_ragged_equals_padded(kind, with_slot):
+    """The same tokens as one ragged batch with padding rows, in an order that is not the sequences'."""
+    st = Setup(kind)
+    from head_wise_kv_b200 import TokenMap
+    lens, counts, n = [0, 200, 40], [260, 1, 33], 260
+    q0, k0, v0 = _qkv(st, 0, 3, (st.B, 200))
+    for c in st.caches:
+        c.append_rope(0, st.rope, None, k0, v0, torch.zeros(3, dtype=torch.int32, device=DEV),
+                      n_new=torch.tensor(lens, dtype=torch.int32, device=DEV))
+    q, k, v = _qkv(st, 0, 4, (st.B, n))
+    T = sum(counts) + 9
+    order = [(b, i) for b in (2, 0, 1) for i in range(counts[b])] + [(-1, 0)] * 9
+    m = TokenMap(st.B, T, DEV)
+    table = st.caches[0]._page_table
+    seq = torch.tensor([b for b, _ in order], dtype=torch.int32)
+    pos = torch.tensor([lens[b] + i if b >= 0 else -1 for b, i in order], dtype=torch.int32)
+    if table is not None:
+        slot = [int(table[b, (lens[b] + i) // PAGE]) * PAGE + (lens[b] + i) % PAGE if b >= 0 else -1 for b, i in order]
+    else:
+        slot = [b * 1500 + lens[b] + i if b >= 0 else -1 for b, i in order]
+    m.seq.copy_(seq), m.pos.copy_(pos), m.slot.copy_(torch.tensor(slot))
+    m.len_after.copy_(torch.tensor([a + b for a, b in zip(lens, counts)], dtype=torch.int32))
+    at = torch.tensor([b for b, _ in order]), torch.tensor([i for _, i in order])
+    before = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    out = torch.full((T, st.hq, st.d), 3.0, dtype=torch.bfloat16, device=DEV)
+    rows = [t[at[0].to(DEV), at[1].to(DEV)].contiguous() for t in (q, k, v)]
+    if not with_slot:
+        m.slot = torch.zeros(0, dtype=torch.int64, device=DEV)      # a NULL pointer: read through the page table
+        assert m.slot.data_ptr() == 0
+    st.caches[0].append_rope(0, st.rope, *rows, before, m, out=out)
+    want = st.caches[1].append_rope(0, st.rope, q, k, v, before,
+                                    n_new=torch.tensor(counts, dtype=torch.int32, device=DEV))
+    assert (out[-9:] == 3).all()
+    assert torch.equal(out[:-9], want[at[0][:-9].to(DEV), at[1][:-9].to(DEV)])
+    assert torch.equal(st.caches[0].buf, st.caches[1].buf)
+    assert st.caches[0].status() == 0
+
+
+def test_all_heads_of_one_kind_and_keys_only():
+    for mask in ([1, 1, 1, 1], [0, 0, 0, 0]):
+        st = Setup("bf16", mask=mask, window=1, sink=0)
+        _, k, v = _qkv(st, 0, 11, (3, 10))
+        counts = [10, 3, 0]
+        assert st.caches[0].append_rope(0, st.rope, None, k, v, torch.zeros(3, dtype=torch.int32, device=DEV),
+                                        n_new=torch.tensor(counts, dtype=torch.int32, device=DEV)) is None
+        _twin_append(st, st.caches[1], k, v, [0, 0, 0], counts, 10)
+        _compare(st, k, [0, 0, 0], counts)
+
+
+def test_status_bits_and_untouched_rows():
+    from head_wise_kv_b200 import TokenMap, _lib as L
+    st = Setup("paged_bf16", caches=1)
+    cache = st.caches[0]
+    q, k, v = _qkv(st, 8, 5)
+    start = cache.buf.clone()
+    zero = torch.zeros(3, dtype=torch.int32, device=DEV)
+
+    def run(seq, pos, slot):
+        cache.buf.copy_(start)
+        m = TokenMap(3, 8, DEV)
+        m.seq[0], m.pos[0], m.slot[0] = seq, pos, slot
+        m.len_after.fill_(pos + 1 if pos >= 0 else 0)
+        cache.append_rope(0, st.rope, q, k, v, zero, m)
+        return cache.status()
+    assert run(3, 0, 0) == L.DUO_STATUS_BAD_LENGTH
+    assert run(0, -2, 0) == L.DUO_STATUS_BAD_LENGTH
+    assert run(0, 1500, 0) == L.DUO_STATUS_OVER_CAPACITY
+    assert run(0, 5, -1) == L.DUO_STATUS_NO_PAGE
+    assert run(0, 5, 20 * PAGE) == L.DUO_STATUS_NO_PAGE
+    assert run(0, 5, 1 << 40) == L.DUO_STATUS_NO_PAGE
+    assert run(-1, 0, 0) == 0
+    # padded: a negative length and one beyond the capacity
+    cache.append_rope(0, st.rope, None, *[t.view(3, 2, *t.shape[1:]) for t in (k[:6], v[:6])],
+                      torch.tensor([-1, 0, 1499], dtype=torch.int32, device=DEV))
+    assert cache.status() == L.DUO_STATUS_BAD_LENGTH | L.DUO_STATUS_OVER_CAPACITY
+
+
+def test_refusals():
+    from head_wise_kv_b200 import DuoError, Rope, TokenMap
+    st = Setup("bf16", caches=1)
+    c = st.caches[0]
+    q, k, v = _qkv(st, 6, 5)
+    zero = torch.zeros(3, dtype=torch.int32, device=DEV)
+    m = TokenMap(3, 6, DEV)
+    q2, k2, v2 = (t.reshape(3, 2, *t.shape[1:]) for t in (q, k, v))
+    for bad in (lambda: c.append_rope(0, Rope(64), q, k, v, zero, m), lambda: c.append_rope(0, st.rope, q, k, v, zero),
+                lambda: c.append_rope(0, st.rope, q, k, v, zero, TokenMap(4, 6, DEV)),
+                lambda: c.append_rope(0, st.rope, q[:5], k, v, zero, m),
+                lambda: c.append_rope(0, st.rope, q, k, v, zero, m, n_new=zero),
+                lambda: c.append_rope(0, st.rope, q, k, v, zero[:2], m),
+                lambda: c.append_rope(0, st.rope, q2.transpose(0, 1).contiguous().transpose(0, 1), k2, v2, zero),
+                lambda: c.append_rope(0, st.rope, None, k, v, zero, m, out=q)):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(TypeError):
+        c.append_rope(0, st.rope, q.float(), k, v, zero, m)
+    off = torch.zeros(6, st.n_kv, st.d + 4, dtype=torch.bfloat16, device=DEV)[..., 4:]
+    with pytest.raises(DuoError) as e:
+        c.append_rope(0, st.rope, q, off, v, zero, m)
+    assert e.value.code == -6
+    with pytest.raises(DuoError):
+        c.append_rope(1, st.rope, q, k, v, zero, m)
+    page = Setup("paged_bf16", caches=1).caches[0]
+    from head_wise_kv_b200 import DuoKVCache
+    bare = DuoKVCache(1, 3, 8, 4, 128, 4, 33, 1500, st.mask[None], device=DEV, page_tokens=PAGE, num_pages=9)
+    with pytest.raises(DuoError):        # no page table
+        bare.append_rope(0, st.rope, None, k2, v2, zero)
+    assert page.status() == 0
+
+
+class _Rows:
+    """Keys and values of every sequence as appended, for the oracle."""
+
+    def __init__(self, st):
+        self.st, self.k, self.v = st, [[] for _ in range(st.B)], [[] for _ in range(st.B)]
+
+    def add(self, b, k, v, first):
+        st = self.st
+        for i in range(k.shape[0]):
+            kk = torch.from_numpy(st.rotate(k[i], first + i)).to(torch.bfloat16).double().numpy()
+            vv = v[i].double().cpu().numpy()
+            if st.kv == "fp8":
+                kk = np.stack([O.dequantize_kv(O.quantize_kv(kk[g], float(st.ks[0, g])), float(st.ks[0, g]))
+                               for g in range(st.n_kv)])
+                vv = np.stack([O.dequantize_kv(O.quantize_kv(vv[g], float(st.vs[0, g])), float(st.vs[0, g]))
+                               for g in range(st.n_kv)])
+            self.k[b].append(kk)
+            self.v[b].append(vv)
+
+    def hist(self, which, b, g):
+        return np.stack([r[g] for r in which[b]])
+
+
+@pytest.mark.parametrize("kind,d", [("bf16", 128), ("paged_bf16", 128), ("fp8", 128), ("bf16", 64)])
+def test_step_rope_equals_append_rope_then_decode(kind, d):
+    st = Setup(kind, B=4, d=d, window=8, layout="interleaved", rot=64)
+    lens = [0, 3, 700, 41]
+    _, k0, v0 = _qkv(st, 0, 21, (4, 700))
+    for c in st.caches:
+        c.append_rope(0, st.rope, None, k0, v0, torch.zeros(4, dtype=torch.int32, device=DEV),
+                      n_new=torch.tensor(lens, dtype=torch.int32, device=DEV))
+    scale = d ** -0.5
+    for step in range(12):
+        q, k, v = _qkv(st, 4, 30 + step)
+        before = torch.tensor(lens, dtype=torch.int32, device=DEV)
+        grow = [1, 1, 1, 1] if step != 5 else [1, 0, 1, 1]      # a length that does not grow: waits for the append
+        after = torch.tensor([max(a + g, 1) for a, g in zip(lens, grow)], dtype=torch.int32, device=DEV)
+        q_rot = torch.empty_like(q.contiguous())
+        got, lse = st.caches[0].step_rope(0, st.rope, q, k, v, before, after, scale, want_lse=True, q_rot=q_rot)
+        qr = st.caches[1].append_rope(0, st.rope, q[:, None], k[:, None], v[:, None], before)[:, 0].contiguous()
+        ref, ref_lse = st.caches[1].decode(0, qr, after, scale, want_lse=True)
+        assert torch.equal(q_rot, qr) and torch.equal(got, ref) and torch.equal(lse, ref_lse)
+        assert torch.equal(st.caches[0].buf, st.caches[1].buf)
+        lens = [a + 1 for a in lens]
+    assert st.caches[0].status() == 0
+
+
+def test_run_of_prompt_chunks_and_steps_against_the_oracle():
+    """prefill_rope in two ragged chunks, then steps: attention equals the oracle on rotated keys."""
+    st = Setup("bf16", B=2, sink=4, window=40, caches=1)
+    cache, rows, scale = st.caches[0], _Rows(st), st.d ** -0.5
+    lens = [0, 0]
+    for C, counts in ((150, [150, 90]), (70, [1, 70])):
+        q, k, v = _qkv(st, 0, 50 + C, (2, C))
+        out = cache.prefill_rope(0, st.rope, q, k, v, torch.tensor(lens, dtype=torch.int32, device=DEV), scale,
+                                 n_new=torch.tensor(counts, dtype=torch.int32, device=DEV))
+        for b, n in enumerate(counts):
+            rows.add(b, k[b, :n], v[b, :n], lens[b])
+            qr = torch.from_numpy(st.rotate(q[b, :n], lens[b] + np.arange(n)[:, None])).to(torch.bfloat16)
+            ref = O.prefill_attention(qr.transpose(0, 1)[None].double().numpy(), lambda _, g: rows.hist(rows.k, b, g),
+                                      lambda _, g: rows.hist(rows.v, b, g), [lens[b]], st.mask, st.S, st.W, scale)
+            assert_close(out[b:b + 1, :, :n].double().cpu().numpy(), ref, f"chunk of {C}, sequence {b}")
+        lens = [a + b for a, b in zip(lens, counts)]
+    for step in range(3):
+        q, k, v = _qkv(st, 2, 90 + step)
+        out = cache.step_rope(0, st.rope, q, k, v, torch.tensor(lens, dtype=torch.int32, device=DEV),
+                              torch.tensor([n + 1 for n in lens], dtype=torch.int32, device=DEV), scale)
+        for b in range(2):
+            rows.add(b, k[b:b + 1], v[b:b + 1], lens[b])
+        qr = np.stack([torch.from_numpy(st.rotate(q[b], lens[b])).to(torch.bfloat16).double().numpy() for b in range(2)])
+        lens = [n + 1 for n in lens]
+        ref, _ = O.decode_attention(qr, lambda b, g: rows.hist(rows.k, b, g), lambda b, g: rows.hist(rows.v, b, g),
+                                    lens, st.mask, st.S, st.W, scale)
+        assert_close(out.double().cpu().numpy(), ref, f"step {step}")
+    assert cache.status() == 0
+
+
+def test_captured_steps():
+    """reserve, append_rope and decode of a step captured once and replayed with lengths that grow on the device."""
+    from head_wise_kv_b200 import TokenMap
+    B = 4
+    st = Setup("paged_bf16", B=B, window=8, cap=600, caches=2)
+    scale = st.d ** -0.5
+    for c in st.caches:
+        c.manage_pages()
+    q, k, v = (t.contiguous() for t in _qkv(st, B, 1))
+    lens = torch.tensor([0, 250, 255, 10], dtype=torch.int32, device=DEV)
+    _, k0, v0 = _qkv(st, 0, 2, (B, 255))
+    for c in st.caches:
+        c.reserve(torch.zeros_like(lens), lens)
+        c.append_rope(0, st.rope, None, k0, v0, torch.zeros_like(lens), n_new=lens)
+    tokens = TokenMap(B, B, DEV)
+    out = torch.empty(B, st.hq, st.d, dtype=torch.float32, device=DEV)
+    q_out = torch.empty_like(q)
+    moving = lens.clone()
+
+    def step():
+        st.caches[0].reserve(moving, None, tokens)
+        st.caches[0].append_rope(0, st.rope, q, k, v, moving, tokens, out=q_out)
+        st.caches[0].decode(0, q_out, tokens.len_after, scale, out=out)
+        moving.add_(1)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for i in range(8):
+        for t in (q, k, v):
+            t.copy_(torch.randn(t.shape, generator=torch.Generator().manual_seed(i)))
+        graph.replay()
+        after = st.caches[1].reserve(lens)
+        ref = st.caches[1].step_rope(0, st.rope, q, k, v, lens, after, scale)
+        lens = after
+        assert torch.equal(out, ref) and torch.equal(tokens.len_after, after)
+    assert st.caches[0].status() == st.caches[1].status() == 0
+    assert torch.equal(st.caches[0].page_state()["table"], st.caches[1].page_state()["table"])
