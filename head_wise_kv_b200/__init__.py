@@ -4,11 +4,12 @@ thin Python binding.
 
 ``DuoKVCache`` owns the cache as a torch buffer and calls the library;
 ``Rope`` rotates queries and keys, ``TokenMap`` holds a step's token map;
+``window_attention`` is the differentiable attention of whole sequences;
 ``_lib`` exposes the C functions one to one.  Both load libduo_kv.so on first
 use and raise ImportError if it is missing (build it with
 ``python -m head_wise_kv_b200.build``); there is no fallback path.
 """
-__all__ = ["DuoKVCache", "DuoError", "Rope", "TokenMap"]
+__all__ = ["DuoKVCache", "DuoError", "Rope", "TokenMap", "window_attention", "window_attention_status"]
 
 
 def __getattr__(name):
@@ -21,6 +22,9 @@ def __getattr__(name):
     if name == "Rope":
         from .rope import Rope
         return Rope
+    if name in ("window_attention", "window_attention_status"):
+        from . import attention
+        return getattr(attention, name)
     if name == "DuoError":
         from ._lib import DuoError
         return DuoError

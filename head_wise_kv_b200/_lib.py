@@ -62,6 +62,7 @@ EXPORTED = (
     "duo_kv_fork", "duo_kv_check_wait_timeout", "duo_decode_step",
     "duo_rope_create", "duo_rope_free", "duo_rope_frequencies", "duo_rope_apply", "duo_kv_append_rope",
     "duo_decode_step_rope", "duo_kv_pages_bytes", "duo_kv_pages_init", "duo_kv_pages_view_get", "duo_kv_reserve",
+    "duo_window_attn_stats_bytes", "duo_window_attn_workspace_bytes", "duo_window_attn", "duo_window_attn_grad",
 )
 DUO_STATIC_WS_BYTES = 4 << 20
 
@@ -145,6 +146,25 @@ class duo_kv_pages_view(ctypes.Structure):
     _fields_ = [("table", _P), ("held", _P), ("refs", _P), ("free_bits", _P), ("max_pages", _I32)]
 
 
+class duo_heads(ctypes.Structure):
+    _fields_ = [("data", _P), ("batch_stride", _I64), ("head_stride", _I64), ("token_stride", _I64)]
+
+
+class duo_window_attn_desc(ctypes.Structure):
+    _fields_ = [
+        ("dtype", _I32),
+        ("batch", _I32),
+        ("num_q_heads", _I32),
+        ("num_kv_heads", _I32),
+        ("head_dim", _I32),
+        ("tokens", _I32),
+        ("sink", _I32),
+        ("window", _I32),
+        ("scale", ctypes.c_float),
+        ("lengths", _P),
+    ]
+
+
 def _sig(name, args, res=ctypes.c_int):
     f = getattr(_lib, name)
     f.argtypes = args
@@ -183,6 +203,10 @@ _c_pages_bytes = _sig("duo_kv_pages_bytes", [_P, _I32, ctypes.POINTER(_SZ)])
 _c_pages_init = _sig("duo_kv_pages_init", [_P, _I32, _P, _SZ, _P])
 _c_pages_view = _sig("duo_kv_pages_view_get", [_P, ctypes.POINTER(duo_kv_pages_view)])
 _c_reserve = _sig("duo_kv_reserve", [_P, _P, _P, _I32, _P, _P, _P, _P, _P, _P])
+_c_win_stats = _sig("duo_window_attn_stats_bytes", [_P, ctypes.POINTER(_SZ)])
+_c_win_ws = _sig("duo_window_attn_workspace_bytes", [_P, ctypes.POINTER(_SZ)])
+_c_win = _sig("duo_window_attn", [_P] * 8)
+_c_win_grad = _sig("duo_window_attn_grad", [_P] * 11 + [_SZ, _P, _P])
 _c_strerror = _sig("duo_strerror", [ctypes.c_int], ctypes.c_char_p)
 
 
@@ -389,3 +413,27 @@ def duo_kv_pages_view_get(handle) -> duo_kv_pages_view:
 
 def duo_kv_reserve(handle, len_before, n_new, map_tokens, len_after, cu, seq, pos, slot, stream) -> None:
     _check(_c_reserve(handle, len_before, n_new, map_tokens, len_after, cu, seq, pos, slot, stream), "duo_kv_reserve")
+
+
+def duo_window_attn_stats_bytes(desc) -> int:
+    n = _SZ(0)
+    _check(_c_win_stats(_ref(desc), ctypes.byref(n)), "duo_window_attn_stats_bytes")
+    return n.value
+
+
+def duo_window_attn_workspace_bytes(desc) -> int:
+    n = _SZ(0)
+    _check(_c_win_ws(_ref(desc), ctypes.byref(n)), "duo_window_attn_workspace_bytes")
+    return n.value
+
+
+def duo_window_attn(desc, q, k, v, out, stats, status, stream) -> None:
+    """q, k, v, out: duo_heads."""
+    _check(_c_win(_ref(desc), _ref(q), _ref(k), _ref(v), _ref(out), stats, status, stream), "duo_window_attn")
+
+
+def duo_window_attn_grad(desc, q, k, v, out, dout, stats, dq, dk, dv, workspace, workspace_bytes, status,
+                         stream) -> None:
+    """q .. dout, dq, dk, dv: duo_heads."""
+    _check(_c_win_grad(_ref(desc), _ref(q), _ref(k), _ref(v), _ref(out), _ref(dout), stats, _ref(dq), _ref(dk),
+                       _ref(dv), workspace, workspace_bytes, status, stream), "duo_window_attn_grad")

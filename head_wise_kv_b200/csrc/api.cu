@@ -15,7 +15,6 @@
 namespace {
 
 constexpr size_t kAlign = 256;
-constexpr unsigned long long kWaitLimitNs = 1000000000ull;   // 1 s per pipeline wait
 
 size_t align_up(size_t x) { return (x + kAlign - 1) & ~(kAlign - 1); }
 
@@ -412,7 +411,7 @@ static int decode_setup(duo_kv* kv, int32_t layer, const uint16_t* q, const int3
     p.W = kv->desc.window;
     p.num_ctas = slots - p.B * p.n_kv;
     p.scale_log2 = scale * 1.4426950408889634f;
-    p.timeout_ns = kWaitLimitNs;
+    p.timeout_ns = duo::kWaitLimitNs;
     memcpy(p.rank, L.rank, sizeof p.rank);
     memcpy(p.r_before, L.r_before, sizeof p.r_before);
     memcpy(p.is_r, L.is_r, sizeof p.is_r);
@@ -587,7 +586,7 @@ int duo_prefill_attn(duo_kv* kv, int32_t layer, const uint16_t* q, const uint16_
     a.n_r = L.n_r;
     a.n_s = L.n_s;
     a.scale = scale;
-    a.timeout_ns = kWaitLimitNs;
+    a.timeout_ns = duo::kWaitLimitNs;
     memcpy(a.rank, L.rank, sizeof a.rank);
     memcpy(a.is_r, L.is_r, sizeof a.is_r);
     a.fp8 = kv->fp8;
@@ -618,7 +617,7 @@ int duo_kv_read_status(duo_kv* kv, int32_t* status, int32_t clear, duo_stream_t 
 }
 
 int duo_kv_check_wait_timeout(duo_kv* kv, uint64_t limit_ns, duo_stream_t stream) {
-    if (!kv || limit_ns == 0 || limit_ns > kWaitLimitNs) return DUO_ERR_INVALID_ARG;
+    if (!kv || limit_ns == 0 || limit_ns > duo::kWaitLimitNs) return DUO_ERR_INVALID_ARG;
     return cuda_err(duo::launch_wait_check(kv->status, limit_ns, static_cast<cudaStream_t>(stream)));
 }
 

@@ -12,6 +12,8 @@
 
 namespace duo {
 
+constexpr unsigned long long kWaitLimitNs = 1000000000ull;   // 1 s per pipeline wait
+
 constexpr int kMaxKvHeads = 64;
 
 // One layer's slice of the caller's device buffer (byte offsets from the base).

@@ -1,0 +1,1158 @@
+// Causal attention with a sliding window and sinks, forward and backward, on
+// the 5th-generation tensor cores (tcgen05), for training the two branches of
+// the gated forward: row i of a sequence sees the keys
+//   j <= i with (j < S or j > i - W),          or every j <= i (full branch).
+//
+// Forward:   s_ij = scale q_i.k_j,  p_ij = exp(s_ij) / sum_j exp(s_ij),  o_i = sum_j p_ij v_j.
+// Backward, with g_i the gradient of o_i and D_i = o_i.g_i:
+//   dv_j = sum_i p_ij g_i
+//   ds_ij = p_ij (g_i.v_j - D_i)
+//   dq_i = scale sum_j ds_ij k_j,   dk_j = scale sum_i ds_ij q_i
+// (sums over the query heads that share a key head for dk and dv).
+//
+// Every tile is 128 rows x 128 keys x 128 dims.  p_ij comes back in the
+// backward from the scores and one saved number per row (minus its
+// log2-sum-exp), so nothing of size T^2 is kept.  Only tiles that hold a
+// visible pair are visited.
+//
+// Precision: products take bf16 (fp16) operands and sum in fp32; scores,
+// softmax statistics, sums and D are fp32.  p_ij and ds_ij are rounded to the
+// inputs' type because a tcgen05 product needs both operands in one 16-bit
+// type: relative 2^-9 per element, averaged over the sums, the size of the
+// rounding of the result.
+//
+// No atomics: the backward visits each tile pair twice, once for the key
+// tile's owner (dK, dV) and once for the query tile's (dQ).  That is 7
+// products per pair instead of 5, and every sum is taken in one fixed order.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <math_constants.h>
+#include <stdint.h>
+#include <string.h>
+
+#include <algorithm>
+
+#include "duo_internal.cuh"
+#include "tcgen05.cuh"
+#include "window_attn.cuh"
+
+namespace duo {
+
+namespace {
+
+constexpr int kTile = 128;                    // rows, keys and dims of a tile
+constexpr uint32_t kSlab = 128 * 128;         // bytes: 128 rows x 64 16-bit elements
+constexpr uint32_t kTileBytes = 2 * kSlab;
+constexpr float kNegBig = -1.0e30f;
+constexpr float kRescaleThreshold = 8.0f;     // log2 units
+
+template <typename T>
+struct Elem;
+template <>
+struct Elem<__nv_bfloat16> {
+    static constexpr bool bf16 = true;
+    static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+    static __device__ __forceinline__ float2 wide(uint32_t x) { return bf2_to_f2(x); }
+};
+template <>
+struct Elem<__half> {
+    static constexpr bool bf16 = false;
+    static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+        const __half2 h = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+    static __device__ __forceinline__ float2 wide(uint32_t x) {
+        return __half22float2(*reinterpret_cast<const __half2*>(&x));
+    }
+};
+
+// ------------------------------------------------------------------ small helpers
+__device__ __forceinline__ uint32_t range_bits(int lo, int hi) {      // bits lo .. hi of 0 .. 31
+    lo = max(lo, 0);
+    hi = min(hi, 31);
+    if (lo > hi) return 0u;
+    const uint32_t upto = hi == 31 ? 0xffffffffu : ((2u << hi) - 1u);
+    return upto & ~((1u << lo) - 1u);
+}
+
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
+    unsigned long long av = *reinterpret_cast<unsigned long long*>(&a);
+    unsigned long long bv = *reinterpret_cast<unsigned long long*>(&b);
+    unsigned long long dv;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(dv) : "l"(av), "l"(bv));
+    return *reinterpret_cast<float2*>(&dv);
+}
+
+// Bounded waits of one CTA: the first that runs out marks the CTA, and every
+// role leaves at its next wait.
+struct Waiter {
+    int32_t* status;
+    unsigned long long limit;
+    volatile int* abort_flag;
+
+    __device__ __forceinline__ bool timed(uint32_t bar, uint32_t parity) const {
+        if (*abort_flag) return false;
+        if (mbar_wait(bar, parity, limit)) return true;
+        if (status) set_status(status, DUO_STATUS_WAIT_TIMEOUT);
+        *abort_flag = 1;
+        return false;
+    }
+    // the whole warp: lane 0 waits for it
+    __device__ __forceinline__ bool warp(uint32_t bar, uint32_t parity) const {
+        if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
+        int ok = 1;
+        if ((threadIdx.x & 31) == 0) ok = timed(bar, parity) ? 1 : 0;
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        __syncwarp();
+        return ok != 0;
+    }
+};
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int t, int h, int b,
+                                            uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+        "[%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(t), "r"(h), "r"(b), "r"(bar)
+        : "memory");
+}
+
+// 128 tokens x 128 dims: two 64-dim slabs, 128-byte swizzled.  Tokens behind
+// the tensor's last one arrive as zeros.
+__device__ __forceinline__ void tma_tile(uint32_t dst, const CUtensorMap* map, int t, int h, int b, uint32_t bar) {
+    tma_load_4d(dst, map, 0, t, h, b, bar);
+    tma_load_4d(dst + kSlab, map, 64, t, h, b, bar);
+}
+
+// 128 consecutive floats.
+__device__ __forceinline__ void bulk_row(uint32_t dst, const float* src, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+        "l"(src), "r"(uint32_t(kTile * 4)), "r"(bar)
+        : "memory");
+}
+
+// Rows [first, 128) of a tile become zeros (one warp): a product must not
+// meet what lies behind a sequence's last token, since 0 x NaN is NaN.
+__device__ __forceinline__ void zero_rows(uint32_t tile, int first) {
+    const int lane = threadIdx.x & 31;
+    for (int off = first * 128 + lane * 16; off < int(kSlab); off += 32 * 16) {
+        st_shared_v4(tile + off, make_uint4(0, 0, 0, 0));
+        st_shared_v4(tile + kSlab + off, make_uint4(0, 0, 0, 0));
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+}
+
+// D (+)= A B^T: both tiles with their 128 dims along K.
+__device__ __forceinline__ void mma_dims(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const uint32_t off = (k >> 2) * kSlab + (k & 3) * 32;
+        umma_f16(d, smem_desc(a + off, 16, 1024), smem_desc(b + off, 16, 1024), idesc, k > 0);
+    }
+}
+
+// D (+)= A B: A in TMEM (16-bit pairs, K steps of 8 columns; the second half
+// of K starts at column `second`), B a tile with its 128 rows along K.
+__device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, int second, uint32_t b, uint32_t idesc, bool add) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        umma_f16_ts(d, a + (k >> 2) * second + (k & 3) * 8, smem_desc(b + k * 2048, kSlab, 1024), idesc,
+                    (add || k > 0) ? 1u : 0u);
+}
+
+__device__ __forceinline__ int length_of(const WindowAttnParams& p, int b) {
+    return p.lengths ? min(max(p.lengths[b], 0), p.T) : p.T;
+}
+
+// The key tiles that query tile qt visits, in order: sinks first.
+struct KeyTiles {
+    int lo, sinks, n;
+    __device__ __forceinline__ KeyTiles(const WindowAttnParams& p, int qt) {
+        lo = p.full ? 0 : max(0, qt * kTile - p.W + 1) / kTile;
+        sinks = p.full ? 0 : min((p.S + kTile - 1) / kTile, lo);
+        n = sinks + qt - lo + 1;
+    }
+    __device__ __forceinline__ int at(int j) const { return j < sinks ? j : lo + j - sinks; }
+};
+
+// Whether every row of query tile qt sees every key of key tile kt < qt.
+__device__ __forceinline__ bool whole(const WindowAttnParams& p, int qt, int kt) {
+    return p.full || kt * kTile + kTile - 1 < p.S || kt * kTile > qt * kTile + kTile - 1 - p.W;
+}
+
+// Keys first .. first + 31 that row i sees.
+__device__ __forceinline__ uint32_t row_sees(const WindowAttnParams& p, int i, int first) {
+    const uint32_t causal = range_bits(0, i - first);
+    if (p.full) return causal;
+    return causal & (range_bits(i - p.W + 1 - first, 31) | range_bits(0, p.S - 1 - first));
+}
+
+// Eight results of a row -> 16 bytes in the tensor's type.
+template <typename T>
+__device__ __forceinline__ uint4 pack8(const uint32_t* u, float f) {
+    uint32_t w[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+        w[x] = Elem<T>::pack(__uint_as_float(u[2 * x]) * f, __uint_as_float(u[2 * x + 1]) * f);
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <typename T>
+__device__ __forceinline__ T* row_at(const HeadTensor& x, int b, int h, int t) {
+    return static_cast<T*>(x.data) + b * x.b + h * x.h + t * x.t;
+}
+
+// ------------------------------------------------------------------ forward
+// One CTA per (sequence, query head, query tile), 6 warps; two CTAs share an
+// SM, so that one's products run under the other's softmax, and one's
+// start and end under the other's middle.
+//   warp 0: TMA (Q once, K and V tiles one ahead)
+//   warp 1: products: S_j = Q K_j^T, O += P_j V_j (P_j from TMEM)
+//   warps 2-5: softmax, a thread per row: running maximum with lazy
+//     rescaling (O is rescaled only where the maximum grows by more than
+//     2^8), P_j over S_j in TMEM, O / l at the end.
+constexpr int kFwdThreads = 192;
+constexpr uint32_t kFwdSmem = 3 * kTileBytes + 1024;
+constexpr uint32_t kFwdCols = 256, kFwdS = 0, kFwdO = 128;
+
+template <typename T>
+__global__ void __launch_bounds__(kFwdThreads, 2) window_fwd_kernel(const __grid_constant__ WindowAttnParams p) {
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ __align__(8) uint64_t q_full, k_full, k_empty, v_full, v_empty, s_full, p_full, done;
+    __shared__ uint32_t tmem_sh;
+    __shared__ int abort_sh;
+    constexpr uint32_t kQK = idesc_f16(kTile, kTile, Elem<T>::bf16, false, false);
+    constexpr uint32_t kPV = idesc_f16(kTile, kTile, Elem<T>::bf16, false, true);
+    const uint32_t sQ = (smem_addr(smem_raw) + 1023) & ~1023u, sK = sQ + kTileBytes, sV = sK + kTileBytes;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+    // the query tiles with most keys first
+    const int heads = p.B * p.hq;
+    const int qt = p.n_t - 1 - int(blockIdx.x) / heads;
+    const int b = int(blockIdx.x) % heads / p.hq, h = int(blockIdx.x) % p.hq, g = h / p.G;
+    const int len = length_of(p, b), i0 = qt * kTile;
+    if (i0 >= len) {        // no row of a sequence: zeros
+        for (int x = threadIdx.x; x < kTile * 16; x += kFwdThreads) {
+            const int t = i0 + x / 16;
+            if (t < p.T) *reinterpret_cast<uint4*>(row_at<T>(p.out, b, h, t) + x % 16 * 8) = make_uint4(0, 0, 0, 0);
+        }
+        if (threadIdx.x < kTile) p.stats[(int64_t(b) * p.hq + h) * p.Tp + i0 + threadIdx.x] = -CUDART_INF_F;
+        return;
+    }
+    const KeyTiles tiles(p, qt);
+    const bool cut = i0 + kTile > len && len < p.T;     // the last key tile reaches behind the sequence
+
+    if (threadIdx.x == 0) {
+        for (uint64_t* bar : {&q_full, &k_full, &k_empty, &v_full, &v_empty, &s_full, &done})
+            mbar_init(smem_addr(bar), 1);
+        mbar_init(smem_addr(&p_full), 4);
+        abort_sh = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) tmem_alloc(smem_addr(&tmem_sh), kFwdCols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_sh;
+    const Waiter wait{p.status, p.timeout_ns, &abort_sh};
+
+    if (warp == 0) {
+        if (lane == 0) {
+            mbar_arrive_expect_tx(smem_addr(&q_full), kTileBytes);
+            tma_tile(sQ, &p.tm_q, i0, h, b, smem_addr(&q_full));
+            int ks = 0, vs = 0;
+            for (int j = 0; j < tiles.n; ++j) {
+                const int t = tiles.at(j) * kTile;
+                if (!wait.timed(smem_addr(&k_empty), (j & 1) ^ 1)) break;
+                mbar_arrive_expect_tx(smem_addr(&k_full), kTileBytes);
+                tma_tile(sK, &p.tm_k, t, g, b, smem_addr(&k_full));
+                ++ks;
+                if (!wait.timed(smem_addr(&v_empty), (j & 1) ^ 1)) break;
+                mbar_arrive_expect_tx(smem_addr(&v_full), kTileBytes);
+                tma_tile(sV, &p.tm_v, t, g, b, smem_addr(&v_full));
+                ++vs;
+            }
+            // no copy may land after this CTA has left
+            mbar_wait(smem_addr(&q_full), 0, p.timeout_ns);
+            if (ks > 0) mbar_wait(smem_addr(&k_full), (ks - 1) & 1, p.timeout_ns);
+            if (vs > 0) mbar_wait(smem_addr(&v_full), (vs - 1) & 1, p.timeout_ns);
+        }
+    } else if (warp == 1) {
+        bool ok = wait.warp(smem_addr(&q_full), 0);
+        for (int j = 0; ok && j < tiles.n; ++j) {
+            // S_j takes the place of P_{j-1}: the products run in the order of issue
+            ok = wait.warp(smem_addr(&k_full), j & 1);
+            if (!ok) break;
+            if (lane == 0) {
+                mma_dims(tmem + kFwdS, sQ, sK, kQK);
+                umma_commit(smem_addr(&s_full));
+                umma_commit(smem_addr(&k_empty));
+            }
+            __syncwarp();
+            ok = wait.warp(smem_addr(&v_full), j & 1);
+            if (!ok) break;
+            if (cut && j == tiles.n - 1) zero_rows(sV, len - i0);
+            ok = wait.warp(smem_addr(&p_full), j & 1);
+            if (!ok) break;
+            tc_fence_after();
+            if (lane == 0) {
+                mma_rows(tmem + kFwdO, tmem + kFwdS, 32, sV, kPV, j > 0);
+                umma_commit(smem_addr(&v_empty));
+            }
+            __syncwarp();
+        }
+        if (lane == 0) {
+            umma_commit(smem_addr(&done));
+            mbar_wait(smem_addr(&done), 0, p.timeout_ns);
+        }
+        __syncwarp();
+    } else {
+        const int quarter = warp & 3, r = quarter * 32 + lane, i = i0 + r;
+        const uint32_t at = tmem + (uint32_t(quarter * 32) << 16);
+        float m = kNegBig, l = 0.f;
+        bool ok = true;
+        for (int j = 0; j < tiles.n; ++j) {
+            ok = wait.warp(smem_addr(&s_full), j & 1);
+            if (!ok) break;
+            tc_fence_after();
+            float s[128];
+            uint32_t* u = reinterpret_cast<uint32_t*>(s);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) tmem_ld32p(at + kFwdS + q * 32, u + q * 32);
+            tmem_wait_ld();
+            const int kt = tiles.at(j);
+            if (kt == qt || !whole(p, qt, kt)) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const uint32_t keep = row_sees(p, i, kt * kTile + q * 32);
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) s[q * 32 + c] = (keep >> c) & 1u ? s[q * 32 + c] : -CUDART_INF_F;
+                }
+            }
+            float t8[8];
+#pragma unroll
+            for (int x = 0; x < 8; ++x) t8[x] = s[x];
+#pragma unroll
+            for (int c = 8; c < 128; c += 2) t8[(c >> 1) & 7] = fmax3(t8[(c >> 1) & 7], s[c], s[c + 1]);
+            const float mx = fmax3(fmax3(t8[0], t8[1], t8[2]), fmax3(t8[3], t8[4], t8[5]), fmaxf(t8[6], t8[7]));
+            const float mt = mx * p.scale_log2;          // a scale above zero keeps the order
+            const bool grow = mt > m + kRescaleThreshold;
+            const float m_new = grow ? mt : m;
+            const float alpha = fast_exp2(m - m_new);
+            m = m_new;
+            // s_full follows O += P_{j-1} V_{j-1} in the order of issue
+            if (j > 0 && __any_sync(0xffffffffu, grow)) {
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t o[32];
+                    tmem_ld32(at + kFwdO + c * 32, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * alpha);
+                    tmem_st32(at + kFwdO + c * 32, o);
+                }
+            }
+            float2 acc[4] = {};
+            const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nm2 = make_float2(-m, -m);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                uint32_t ph[16];
+#pragma unroll
+                for (int c = 0; c < 32; c += 2) {
+                    const float2 x = ffma2(make_float2(s[q * 32 + c], s[q * 32 + c + 1]), sc2, nm2);
+                    const float2 e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+                    acc[(c >> 1) & 3] = fadd2(acc[(c >> 1) & 3], e);
+                    ph[c / 2] = Elem<T>::pack(e.x, e.y);
+                }
+                tmem_stn<16>(at + kFwdS + q * 16, ph);
+            }
+            const float2 sum = fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3]));
+            l = l * alpha + (sum.x + sum.y);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&p_full));
+        }
+        if (ok) ok = wait.warp(smem_addr(&done), 0);
+        if (ok) {
+            tc_fence_after();
+            const bool row = i < len;
+            const float inv = row && l > 0.f ? 1.f / l : 0.f;
+            p.stats[(int64_t(b) * p.hq + h) * p.Tp + i] = row && l > 0.f ? -(m + __log2f(l)) : -CUDART_INF_F;
+            T* dst = row_at<T>(p.out, b, h, i);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t o[32];
+                tmem_ld32(at + kFwdO + c * 32, o);
+                tmem_wait_ld();
+                if (i < p.T) {
+#pragma unroll
+                    for (int x = 0; x < 32; x += 8)
+                        *reinterpret_cast<uint4*>(dst + c * 32 + x) = row ? pack8<T>(o + x, inv) : make_uint4(0, 0, 0, 0);
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kFwdCols);
+    }
+}
+
+// ------------------------------------------------------------------ D_i = o_i . g_i
+// Bound by HBM: reads each output and gradient row once.  16 threads per row.
+template <typename T>
+__global__ void __launch_bounds__(256) window_delta_kernel(const __grid_constant__ WindowAttnParams p) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+    const int64_t row = (int64_t(blockIdx.x) * 256 + threadIdx.x) / 16;
+    const int part = threadIdx.x % 16;
+    if (row >= int64_t(p.B) * p.hq * p.Tp) return;
+    const int64_t bh = row / p.Tp;
+    const int t = int(row - bh * p.Tp), b = int(bh / p.hq), h = int(bh - int64_t(b) * p.hq);
+    float d = 0.f;
+    if (t < length_of(p, b)) {
+        const uint4 x = *reinterpret_cast<const uint4*>(row_at<const T>(p.out, b, h, t) + part * 8);
+        const uint4 y = *reinterpret_cast<const uint4*>(row_at<const T>(p.dout, b, h, t) + part * 8);
+        const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float2 u = Elem<T>::wide(xs[k]), v = Elem<T>::wide(ys[k]);
+            d = fmaf(u.x, v.x, fmaf(u.y, v.y, d));
+        }
+    }
+#pragma unroll
+    for (int k = 8; k > 0; k >>= 1) d += __shfl_xor_sync(0xffffffffu, d, k);
+    if (part == 0) p.delta[row] = d;
+}
+
+// ------------------------------------------------------------------ backward
+// 10 warps: 0-7 elementwise (two per TMEM lane quarter, one 64-column half
+// each), 8 TMA, 9 products.  One launch holds two kinds of work items: first
+// those of the key tiles (the longest), then those of the query tiles, which
+// fill the SMs that have run out of the first.
+constexpr int kBwdThreads = 320;
+constexpr uint32_t kBwdSmem = 6 * kTileBytes + 4 * kTile * 4 + 1024;
+constexpr uint32_t kBwdCols = 512;
+
+struct BwdShared {
+    uint64_t once, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full, dp_full, ds_full, done;
+    uint32_t tmem;
+    int abort_flag;
+};
+
+// What a key tile's work item is: rows x of its list of (query head of the
+// group, query tile), x0 <= x < x1.
+struct KeyItem {
+    int b, g, kt, pieces, piece;
+    int nq;              // query tiles that see the key tile
+    int x0, x1;
+    int64_t slot;        // of its partial sums
+    __device__ __forceinline__ KeyItem(const WindowAttnParams& p, int item) {
+        const int bk = p.B * p.n_kv, first = p.n_long * p.p_long * bk;
+        const bool lng = item < first;
+        pieces = lng ? p.p_long : p.p_short;
+        const int x = lng ? item : item - first;
+        kt = x / (pieces * bk) + (lng ? 0 : p.n_long);
+        piece = x / bk % pieces;
+        b = x % bk / p.n_kv;
+        g = x % p.n_kv;
+        slot = lng || p.p_long == 1 ? x : int64_t(first) + x;      // a class of one piece has no slots
+        const int len = length_of(p, b);
+        int hi = (len - 1) / kTile;                      // -1 / 128 is 0: an empty sequence has no rows below
+        if (!p.full && kt * kTile >= p.S) hi = min(hi, (kt * kTile + kTile - 1 + p.W - 1) / kTile);
+        nq = len > kt * kTile ? hi - kt + 1 : 0;
+        const int64_t all = int64_t(nq) * p.G;
+        x0 = int(all * piece / pieces);
+        x1 = int(all * (piece + 1) / pieces);
+    }
+};
+
+// Key tile: K, V stay; Q and g tiles pass.  With keys along the TMEM lanes,
+//   S^T = K Q^T, P^T = exp2(..) over S^T,  dP^T = V g^T, dS^T over dP^T,
+//   dV += P^T g,  dK += dS^T Q
+// P^T and dS^T are the A operands of the second pair straight from TMEM.
+// The products of one phase run under the elementwise work of the other:
+// dV_x and S_{x+1} while dS_x is worked out, dK_x and dP_{x+1} while P_{x+1} is.
+template <typename T>
+__device__ __forceinline__ void key_tile(const WindowAttnParams& p, BwdShared& sh, uint32_t smem, const Waiter& wait) {
+    constexpr uint32_t kDims = idesc_f16(kTile, kTile, Elem<T>::bf16, false, false);
+    constexpr uint32_t kRows = idesc_f16(kTile, kTile, Elem<T>::bf16, false, true);
+    constexpr uint32_t kS = 0, kDP = 128, kDV = 256, kDK = 384;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const KeyItem it(p, int(blockIdx.x));
+    const uint32_t sK = smem, sV = sK + kTileBytes, sQ = sV + kTileBytes, sG = sQ + 2 * kTileBytes,
+                   sStat = sG + 2 * kTileBytes;       // [stage][stats, delta][128]
+    const int len = length_of(p, it.b), k0 = it.kt * kTile, n = it.x1 - it.x0;
+    const uint32_t tmem = sh.tmem;
+
+    if (warp == 8) {
+        if (lane == 0 && n > 0) {
+            mbar_arrive_expect_tx(smem_addr(&sh.once), 2 * kTileBytes);
+            tma_tile(sK, &p.tm_k, k0, it.g, it.b, smem_addr(&sh.once));
+            tma_tile(sV, &p.tm_v, k0, it.g, it.b, smem_addr(&sh.once));
+            int x = 0;
+            for (; x < n; ++x) {
+                const int st = x & 1, at = it.x0 + x;
+                const int h = it.g * p.G + at / it.nq, i0 = (it.kt + at % it.nq) * kTile;
+                const uint32_t bar = smem_addr(&sh.k_full[st]);
+                if (!wait.timed(smem_addr(&sh.k_empty[st]), ((x >> 1) & 1) ^ 1)) break;
+                mbar_arrive_expect_tx(bar, 2 * kTileBytes + 2 * kTile * 4);
+                tma_tile(sQ + st * kTileBytes, &p.tm_q, i0, h, it.b, bar);
+                tma_tile(sG + st * kTileBytes, &p.tm_do, i0, h, it.b, bar);
+                const int64_t row = (int64_t(it.b) * p.hq + h) * p.Tp + i0;
+                bulk_row(sStat + st * kTile * 8, p.stats + row, bar);
+                bulk_row(sStat + st * kTile * 8 + kTile * 4, p.delta + row, bar);
+            }
+            mbar_wait(smem_addr(&sh.once), 0, p.timeout_ns);
+            for (int k = 1; k <= 2 && k <= x; ++k)
+                mbar_wait(smem_addr(&sh.k_full[(x - k) & 1]), ((x - k) >> 1) & 1, p.timeout_ns);
+        }
+    } else if (warp == 9) {
+        bool ok = n > 0 && wait.warp(smem_addr(&sh.once), 0);
+        // Q and g of step x, without what lies behind the sequence
+        const auto arrived = [&](int x) {
+            const int st = x & 1, i0 = (it.kt + (it.x0 + x) % it.nq) * kTile;
+            if (!wait.warp(smem_addr(&sh.k_full[st]), (x >> 1) & 1)) return false;
+            if (i0 + kTile > len && len < p.T) {
+                zero_rows(sQ + st * kTileBytes, len - i0);
+                zero_rows(sG + st * kTileBytes, len - i0);
+            }
+            return true;
+        };
+        if (ok) ok = arrived(0);
+        if (ok && lane == 0) {
+            mma_dims(tmem + kS, sK, sQ, kDims);
+            umma_commit(smem_addr(&sh.s_full[0]));
+            mma_dims(tmem + kDP, sV, sG, kDims);
+            umma_commit(smem_addr(&sh.dp_full));
+        }
+        __syncwarp();
+        for (int x = 0; ok && x < n; ++x) {
+            const int st = x & 1, nx = st ^ 1;
+            const bool more = x + 1 < n;
+            ok = wait.warp(smem_addr(&sh.p_full), x & 1);
+            if (!ok) break;
+            tc_fence_after();
+            if (lane == 0) mma_rows(tmem + kDV, tmem + kS, 64, sG + st * kTileBytes, kRows, x > 0);
+            __syncwarp();
+            if (more) {
+                ok = arrived(x + 1);
+                if (!ok) break;
+                if (lane == 0) {
+                    mma_dims(tmem + kS, sK, sQ + nx * kTileBytes, kDims);
+                    umma_commit(smem_addr(&sh.s_full[0]));
+                }
+                __syncwarp();
+            }
+            ok = wait.warp(smem_addr(&sh.ds_full), x & 1);
+            if (!ok) break;
+            tc_fence_after();
+            if (lane == 0) {
+                mma_rows(tmem + kDK, tmem + kDP, 64, sQ + st * kTileBytes, kRows, x > 0);
+                umma_commit(smem_addr(&sh.k_empty[st]));
+                if (more) {
+                    mma_dims(tmem + kDP, sV, sG + nx * kTileBytes, kDims);
+                    umma_commit(smem_addr(&sh.dp_full));
+                }
+            }
+            __syncwarp();
+        }
+        if (lane == 0) {
+            umma_commit(smem_addr(&sh.done));
+            mbar_wait(smem_addr(&sh.done), 0, p.timeout_ns);
+        }
+        __syncwarp();
+    } else {
+        const int quarter = warp & 3, half = warp >> 2, r = quarter * 32 + lane, key = k0 + r, cb = half * 64;
+        const uint32_t at = tmem + (uint32_t(quarter * 32) << 16) + cb;
+        const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
+        bool ok = true;
+        for (int x = 0; x < n; ++x) {
+            const int st = x & 1, qt = it.kt + (it.x0 + x) % it.nq, i0 = qt * kTile;
+            const uint32_t stat = sStat + st * kTile * 8 + cb * 4;
+            // this thread's own wait for the statistics that came with Q and g
+            ok = wait.warp(smem_addr(&sh.k_full[st]), (x >> 1) & 1) && wait.warp(smem_addr(&sh.s_full[0]), x & 1);
+            if (!ok) break;
+            tc_fence_after();
+            float s[64];
+            uint32_t* u = reinterpret_cast<uint32_t*>(s);
+            tmem_ld32p(at + kS, u);
+            tmem_ld32p(at + kS + 32, u + 32);
+            tmem_wait_ld();
+            if (qt == it.kt || !whole(p, qt, it.kt) || i0 + kTile > len) {
+                // rows i0 + c with key <= row < len, within the window unless the key is a sink
+                int hi = len - 1 - i0;
+                if (!p.full && key >= p.S) hi = min(hi, key + p.W - 1 - i0);
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const int o = cb + q * 32;
+                    const uint32_t keep = range_bits(key - i0 - o, hi - o);
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) s[q * 32 + c] = (keep >> c) & 1u ? s[q * 32 + c] : -CUDART_INF_F;
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                uint32_t ph[16];
+#pragma unroll
+                for (int c = 0; c < 32; c += 4) {
+                    const uint4 nl = lds128(stat + (q * 32 + c) * 4);
+                    float* e = s + q * 32 + c;
+                    const float2 a = ffma2(make_float2(e[0], e[1]), sc2,
+                                           make_float2(__uint_as_float(nl.x), __uint_as_float(nl.y)));
+                    const float2 d = ffma2(make_float2(e[2], e[3]), sc2,
+                                           make_float2(__uint_as_float(nl.z), __uint_as_float(nl.w)));
+                    e[0] = fast_exp2(a.x);
+                    e[1] = fast_exp2(a.y);
+                    e[2] = fast_exp2(d.x);
+                    e[3] = fast_exp2(d.y);
+                    ph[c / 2] = Elem<T>::pack(e[0], e[1]);
+                    ph[c / 2 + 1] = Elem<T>::pack(e[2], e[3]);
+                }
+                tmem_stn<16>(at + kS + q * 16, ph);     // over this thread's own columns of S^T
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&sh.p_full));
+            ok = wait.warp(smem_addr(&sh.dp_full), x & 1);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                uint32_t d[32], ph[16];
+                tmem_ld32(at + kDP + q * 32, d);
+                tmem_wait_ld();
+#pragma unroll
+                for (int c = 0; c < 32; c += 4) {
+                    const uint4 dl = lds128(stat + kTile * 4 + (q * 32 + c) * 4);
+                    const float* e = s + q * 32 + c;
+                    ph[c / 2] = Elem<T>::pack(e[0] * (__uint_as_float(d[c]) - __uint_as_float(dl.x)),
+                                              e[1] * (__uint_as_float(d[c + 1]) - __uint_as_float(dl.y)));
+                    ph[c / 2 + 1] = Elem<T>::pack(e[2] * (__uint_as_float(d[c + 2]) - __uint_as_float(dl.z)),
+                                                  e[3] * (__uint_as_float(d[c + 3]) - __uint_as_float(dl.w)));
+                }
+                // over columns 0..31, which this thread has read
+                tmem_stn<16>(at + kDP + q * 16, ph);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&sh.ds_full));
+        }
+        if (ok) ok = wait.warp(smem_addr(&sh.done), 0);
+        if (ok) {
+            tc_fence_after();
+            const bool row = key < len && n > 0;
+            if (it.pieces > 1) {
+                float* dst = p.part + it.slot * (2 * kTile * kTile) + r * kTile + cb;
+#pragma unroll
+                for (int w = 0; w < 2; ++w)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        uint32_t o[32];
+                        tmem_ld32(at + (w ? kDV : kDK) + c * 32, o);
+                        tmem_wait_ld();
+                        float4* y = reinterpret_cast<float4*>(dst + w * kTile * kTile + c * 32);
+#pragma unroll
+                        for (int z = 0; z < 32; z += 4)
+                            y[z / 4] = row ? make_float4(__uint_as_float(o[z]), __uint_as_float(o[z + 1]),
+                                                         __uint_as_float(o[z + 2]), __uint_as_float(o[z + 3]))
+                                           : make_float4(0.f, 0.f, 0.f, 0.f);
+                    }
+            } else {
+#pragma unroll
+                for (int w = 0; w < 2; ++w)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        uint32_t o[32];
+                        tmem_ld32(at + (w ? kDV : kDK) + c * 32, o);
+                        tmem_wait_ld();
+                        if (key < p.T) {
+                            T* dst = row_at<T>(w ? p.dv : p.dk, it.b, it.g, key) + cb + c * 32;
+#pragma unroll
+                            for (int z = 0; z < 32; z += 8)
+                                *reinterpret_cast<uint4*>(dst + z) =
+                                    row ? pack8<T>(o + z, w ? 1.f : p.scale) : make_uint4(0, 0, 0, 0);
+                        }
+                    }
+            }
+        }
+    }
+}
+
+// Query tile: Q, g stay; K and V tiles pass.  With rows along the TMEM lanes,
+//   S = Q K^T (two buffers), dP = g V^T, dS over S, dQ += dS K.
+template <typename T>
+__device__ __forceinline__ void query_tile(const WindowAttnParams& p, BwdShared& sh, uint32_t smem,
+                                           const Waiter& wait) {
+    constexpr uint32_t kDims = idesc_f16(kTile, kTile, Elem<T>::bf16, false, false);
+    constexpr uint32_t kRows = idesc_f16(kTile, kTile, Elem<T>::bf16, false, true);
+    constexpr uint32_t kS = 0, kDP = 256, kDQ = 384;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int item = int(blockIdx.x) - p.items_kv, heads = p.B * p.hq;
+    const int qt = p.n_t - 1 - item / heads, b = item % heads / p.hq, h = item % p.hq, g = h / p.G;
+    const uint32_t sQ = smem, sG = sQ + kTileBytes, sK = sG + kTileBytes, sV = sK + 2 * kTileBytes;
+    const int len = length_of(p, b), i0 = qt * kTile;
+    const KeyTiles tiles(p, qt);
+    const int n = i0 < len ? tiles.n : 0;
+    const bool cut = i0 + kTile > len && len < p.T;
+    const uint32_t tmem = sh.tmem;
+
+    if (warp == 8) {
+        if (lane == 0 && n > 0) {
+            mbar_arrive_expect_tx(smem_addr(&sh.once), 2 * kTileBytes);
+            tma_tile(sQ, &p.tm_q, i0, h, b, smem_addr(&sh.once));
+            tma_tile(sG, &p.tm_do, i0, h, b, smem_addr(&sh.once));
+            int ks = 0, vs = 0;
+            for (int j = 0; j < n; ++j) {
+                const int st = j & 1, t = tiles.at(j) * kTile;
+                const uint32_t parity = ((j >> 1) & 1) ^ 1;
+                if (!wait.timed(smem_addr(&sh.k_empty[st]), parity)) break;
+                mbar_arrive_expect_tx(smem_addr(&sh.k_full[st]), kTileBytes);
+                tma_tile(sK + st * kTileBytes, &p.tm_k, t, g, b, smem_addr(&sh.k_full[st]));
+                ++ks;
+                if (!wait.timed(smem_addr(&sh.v_empty[st]), parity)) break;
+                mbar_arrive_expect_tx(smem_addr(&sh.v_full[st]), kTileBytes);
+                tma_tile(sV + st * kTileBytes, &p.tm_v, t, g, b, smem_addr(&sh.v_full[st]));
+                ++vs;
+            }
+            mbar_wait(smem_addr(&sh.once), 0, p.timeout_ns);
+            for (int k = 1; k <= 2 && k <= ks; ++k)
+                mbar_wait(smem_addr(&sh.k_full[(ks - k) & 1]), ((ks - k) >> 1) & 1, p.timeout_ns);
+            for (int k = 1; k <= 2 && k <= vs; ++k)
+                mbar_wait(smem_addr(&sh.v_full[(vs - k) & 1]), ((vs - k) >> 1) & 1, p.timeout_ns);
+        }
+    } else if (warp == 9) {
+        bool ok = n > 0 && wait.warp(smem_addr(&sh.once), 0);
+        const auto keys = [&](int j) {
+            const uint32_t tile = sK + (j & 1) * kTileBytes;
+            if (!wait.warp(smem_addr(&sh.k_full[j & 1]), (j >> 1) & 1)) return false;
+            if (cut && j == n - 1) zero_rows(tile, len - i0);
+            if (lane == 0) {
+                mma_dims(tmem + kS + (j & 1) * 128, sQ, tile, kDims);
+                umma_commit(smem_addr(&sh.s_full[j & 1]));
+            }
+            __syncwarp();
+            return true;
+        };
+        const auto values = [&](int j) {
+            const uint32_t tile = sV + (j & 1) * kTileBytes;
+            if (!wait.warp(smem_addr(&sh.v_full[j & 1]), (j >> 1) & 1)) return false;
+            if (cut && j == n - 1) zero_rows(tile, len - i0);
+            if (lane == 0) {
+                mma_dims(tmem + kDP, sG, tile, kDims);
+                umma_commit(smem_addr(&sh.dp_full));
+                umma_commit(smem_addr(&sh.v_empty[j & 1]));
+            }
+            __syncwarp();
+            return true;
+        };
+        ok = ok && keys(0) && values(0);
+        for (int j = 0; ok && j < n; ++j) {
+            if (j + 1 < n) ok = keys(j + 1);
+            ok = ok && wait.warp(smem_addr(&sh.ds_full), j & 1);
+            if (!ok) break;
+            tc_fence_after();
+            if (j + 1 < n) ok = values(j + 1);
+            if (!ok) break;
+            if (lane == 0) {
+                mma_rows(tmem + kDQ, tmem + kS + (j & 1) * 128, 64, sK + (j & 1) * kTileBytes, kRows, j > 0);
+                umma_commit(smem_addr(&sh.k_empty[j & 1]));
+            }
+            __syncwarp();
+        }
+        if (lane == 0) {
+            umma_commit(smem_addr(&sh.done));
+            mbar_wait(smem_addr(&sh.done), 0, p.timeout_ns);
+        }
+        __syncwarp();
+    } else {
+        const int quarter = warp & 3, half = warp >> 2, r = quarter * 32 + lane, i = i0 + r, cb = half * 64;
+        const uint32_t at = tmem + (uint32_t(quarter * 32) << 16) + cb;
+        const int64_t row = (int64_t(b) * p.hq + h) * p.Tp + i;
+        const float nl = p.stats[row], dl = p.delta[row];
+        const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nl2 = make_float2(nl, nl);
+        bool ok = true;
+        for (int j = 0; j < n; ++j) {
+            const int kt = tiles.at(j);
+            const uint32_t sb = kS + (j & 1) * 128;
+            ok = wait.warp(smem_addr(&sh.s_full[j & 1]), (j >> 1) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            float s[64];
+            uint32_t* u = reinterpret_cast<uint32_t*>(s);
+            tmem_ld32p(at + sb, u);
+            tmem_ld32p(at + sb + 32, u + 32);
+            tmem_wait_ld();
+            if (kt == qt || !whole(p, qt, kt)) {
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const uint32_t keep = row_sees(p, i, kt * kTile + cb + q * 32);
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) s[q * 32 + c] = (keep >> c) & 1u ? s[q * 32 + c] : -CUDART_INF_F;
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < 64; c += 2) {
+                const float2 a = ffma2(make_float2(s[c], s[c + 1]), sc2, nl2);
+                s[c] = fast_exp2(a.x);
+                s[c + 1] = fast_exp2(a.y);
+            }
+            ok = wait.warp(smem_addr(&sh.dp_full), j & 1);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                uint32_t d[32], ph[16];
+                tmem_ld32(at + kDP + q * 32, d);
+                tmem_wait_ld();
+#pragma unroll
+                for (int c = 0; c < 32; c += 2)
+                    ph[c / 2] = Elem<T>::pack(s[q * 32 + c] * (__uint_as_float(d[c]) - dl),
+                                              s[q * 32 + c + 1] * (__uint_as_float(d[c + 1]) - dl));
+                tmem_stn<16>(at + sb + q * 16, ph);     // over this thread's own columns of S
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&sh.ds_full));
+        }
+        if (ok) ok = wait.warp(smem_addr(&sh.done), 0);
+        if (ok) {
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                uint32_t o[32];
+                tmem_ld32(at + kDQ + c * 32, o);
+                tmem_wait_ld();
+                if (i < p.T) {
+                    T* dst = row_at<T>(p.dq, b, h, i) + cb + c * 32;
+#pragma unroll
+                    for (int z = 0; z < 32; z += 8)
+                        *reinterpret_cast<uint4*>(dst + z) =
+                            i < len ? pack8<T>(o + z, p.scale) : make_uint4(0, 0, 0, 0);
+                }
+            }
+        }
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kBwdThreads, 1) window_bwd_kernel(const __grid_constant__ WindowAttnParams p) {
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ __align__(8) BwdShared sh;
+    const uint32_t smem = (smem_addr(smem_raw) + 1023) & ~1023u;
+    const int warp = threadIdx.x >> 5;
+    if (threadIdx.x == 0) {
+        for (uint64_t* bar : {&sh.once, &sh.k_full[0], &sh.k_full[1], &sh.k_empty[0], &sh.k_empty[1], &sh.v_full[0],
+                              &sh.v_full[1], &sh.v_empty[0], &sh.v_empty[1], &sh.s_full[0], &sh.s_full[1],
+                              &sh.dp_full, &sh.done})
+            mbar_init(smem_addr(bar), 1);
+        mbar_init(smem_addr(&sh.p_full), 8);
+        mbar_init(smem_addr(&sh.ds_full), 8);
+        sh.abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 9) tmem_alloc(smem_addr(&sh.tmem), kBwdCols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+    const Waiter wait{p.status, p.timeout_ns, &sh.abort_flag};
+    if (int(blockIdx.x) < p.items_kv)
+        key_tile<T>(p, sh, smem, wait);
+    else
+        query_tile<T>(p, sh, smem, wait);
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc(sh.tmem, kBwdCols);
+    }
+}
+
+// dK, dV of the key tiles whose rows were shared out: the pieces' sums, in
+// order.  Bound by HBM.  Sixteen blocks per key tile: 16 rows each of dK
+// (first 8), then of dV.
+template <typename T>
+__global__ void __launch_bounds__(256) window_join_kernel(const __grid_constant__ WindowAttnParams p) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+    const int bk = p.B * p.n_kv;
+    const int n_first = p.p_long > 1 ? p.n_long * bk : 0;
+    const int tile = int(blockIdx.x) / 16;
+    const bool lng = tile < n_first;
+    const int y = lng ? tile : tile - n_first, pieces = lng ? p.p_long : p.p_short;
+    const int kt = y / bk + (lng ? 0 : p.n_long), b = y % bk / p.n_kv, g = y % p.n_kv;
+    const int w = blockIdx.x / 8 % 2, r = blockIdx.x % 8 * 16 + threadIdx.x / 16, c = threadIdx.x % 16 * 8;
+    const int key = kt * kTile + r;
+    if (key >= p.T) return;
+    const int64_t first = (lng || p.p_long == 1 ? 0 : int64_t(p.n_long) * p.p_long * bk) +
+                          int64_t(y / bk) * pieces * bk + y % bk;
+    uint32_t o[8] = {};
+    for (int k = 0; k < pieces; ++k) {
+        const float* src = p.part + (first + int64_t(k) * bk) * (2 * kTile * kTile) + w * kTile * kTile + r * kTile + c;
+        const float4 u = reinterpret_cast<const float4*>(src)[0], v = reinterpret_cast<const float4*>(src)[1];
+        const float f[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int z = 0; z < 8; ++z) o[z] = __float_as_uint(__uint_as_float(o[z]) + f[z]);
+    }
+    *reinterpret_cast<uint4*>(row_at<T>(w ? p.dv : p.dk, b, g, key) + c) = pack8<T>(o, w ? 1.f : p.scale);
+}
+
+// ------------------------------------------------------------------ host side
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+int padded(int tokens) { return (tokens + kTile - 1) / kTile * kTile; }
+
+// [batch][heads][tokens][128] by strides; box 64 x 128 tokens, 128-byte swizzle.
+bool make_map(CUtensorMap* m, const duo_heads& x, const duo_window_attn_desc& d, int heads) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return false;
+    const cuuint64_t n[3] = {cuuint64_t(d.tokens), cuuint64_t(heads), cuuint64_t(d.batch)};
+    const int64_t s[3] = {x.token_stride, x.head_stride, x.batch_stride};
+    cuuint64_t dims[4] = {cuuint64_t(kTile), n[0], n[1], n[2]}, strides[3];
+    // a dimension of one entry has no stride that matters
+    for (int i = 0; i < 3; ++i) strides[i] = n[i] > 1 ? cuuint64_t(s[i]) * 2 : kTile * 2;
+    cuuint32_t box[4] = {64, 128, 1, 1}, one[4] = {1, 1, 1, 1};
+    return enc(m, d.dtype == DUO_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, x.data,
+               dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int check_desc(const duo_window_attn_desc* d) {
+    if (!d) return DUO_ERR_INVALID_ARG;
+    if (d->dtype != DUO_BF16 && d->dtype != DUO_FP16) return DUO_ERR_UNSUPPORTED;
+    if (d->head_dim != kTile) return DUO_ERR_UNSUPPORTED;
+    if (d->batch < 0 || d->tokens < 0 || d->num_q_heads < 1 || d->num_kv_heads < 1 ||
+        d->num_q_heads % d->num_kv_heads != 0)
+        return DUO_ERR_INVALID_ARG;
+    if (d->sink < 0 || d->window < 0) return DUO_ERR_INVALID_ARG;
+    if (!(d->scale > 0.f) || !(d->scale < 1e30f)) return DUO_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(d->lengths) & 3) return DUO_ERR_ALIGNMENT;
+    if (d->tokens > (1 << 26)) return DUO_ERR_UNSUPPORTED;
+    // work items are counted in 31 bits, with room for the pieces
+    if (int64_t(d->batch) * d->num_q_heads * (padded(d->tokens) / kTile) > (1 << 26)) return DUO_ERR_UNSUPPORTED;
+    return DUO_OK;
+}
+
+int check_heads(const duo_heads* x, const duo_window_attn_desc& d, int heads) {
+    if (!x || !x->data) return DUO_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(x->data) & 15) return DUO_ERR_ALIGNMENT;
+    const int64_t n[3] = {d.batch, heads, d.tokens}, s[3] = {x->batch_stride, x->head_stride, x->token_stride};
+    for (int i = 0; i < 3; ++i) {
+        if (n[i] <= 1) continue;
+        if (s[i] % 8 != 0) return DUO_ERR_ALIGNMENT;
+        if (s[i] < kTile || s[i] >= (int64_t(1) << 39)) return DUO_ERR_INVALID_ARG;
+    }
+    return DUO_OK;
+}
+
+HeadTensor head_tensor(const duo_heads& x) { return HeadTensor{x.data, x.batch_stride, x.head_stride, x.token_stride}; }
+
+void fill_params(WindowAttnParams& p, const duo_window_attn_desc& d, int32_t* status) {
+    p.B = d.batch;
+    p.hq = d.num_q_heads;
+    p.n_kv = d.num_kv_heads;
+    p.G = p.hq / p.n_kv;
+    p.T = d.tokens;
+    p.Tp = padded(d.tokens);
+    p.n_t = p.Tp / kTile;
+    p.full = d.window == 0 || d.window >= d.tokens;
+    p.W = std::min(p.full ? d.tokens : d.window, d.tokens);
+    p.S = p.full ? 0 : std::min(d.sink, d.tokens);
+    p.scale = d.scale;
+    p.scale_log2 = d.scale * 1.4426950408889634f;
+    p.lengths = d.lengths;
+    p.status = status;
+    p.timeout_ns = kWaitLimitNs;
+}
+
+// How the key tiles' work is shared out.  A key tile's list has (query tiles
+// that see it) x (query heads of the group) entries; those that hold sinks
+// are seen by every later row.  A class of tiles whose longest list is about
+// k times an SM's share of the whole is cut in k pieces, but in none shorter
+// than kPiece entries, which cost more to join than they gain.
+constexpr int kPiece = 8;
+
+void plan_pieces(WindowAttnParams& p, int num_sms) {
+    const auto list = [&](int kt) {
+        int hi = p.n_t - 1;
+        if (!p.full && kt * kTile >= p.S) hi = std::min(hi, int((int64_t(kt) * kTile + kTile - 1 + p.W - 1) / kTile));
+        return int64_t(hi - kt + 1) * p.G;
+    };
+    p.n_long = p.full ? 0 : std::min(p.n_t, (p.S + kTile - 1) / kTile);
+    int64_t all = 0, top_long = 0, top_short = 0;
+    for (int kt = 0; kt < p.n_t; ++kt) {
+        all += list(kt);
+        int64_t& top = kt < p.n_long ? top_long : top_short;
+        top = std::max(top, list(kt));
+    }
+    const int64_t share = std::max<int64_t>(all * p.B * p.n_kv / num_sms, kPiece);
+    const auto pieces = [&](int64_t top) { return int(std::min<int64_t>(std::max<int64_t>((top + share / 2) / share, 1), 64)); };
+    p.p_long = pieces(top_long);
+    p.p_short = pieces(top_short);
+    p.items_kv = (p.n_long * p.p_long + (p.n_t - p.n_long) * p.p_short) * p.B * p.n_kv;
+}
+
+int64_t partial_slots(const WindowAttnParams& p) {
+    const int64_t bk = int64_t(p.B) * p.n_kv;
+    return (p.p_long > 1 ? int64_t(p.n_long) * p.p_long * bk : 0) +
+           (p.p_short > 1 ? int64_t(p.n_t - p.n_long) * p.p_short * bk : 0);
+}
+
+// The current device's SMs.  A thread that has made no call on the device yet
+// (autograd's) has no context for the tensor maps: cudaSetDevice binds it.
+int device_sms(int* sms) {
+    int dev = 0;
+    return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess &&
+                   cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess
+               ? DUO_OK
+               : DUO_ERR_CUDA;
+}
+
+template <typename K>
+cudaError_t launch(K kernel, const WindowAttnParams& p, dim3 grid, int threads, uint32_t smem, cudaStream_t s) {
+    if (smem > 0) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+        if (e != cudaSuccess) return e;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(unsigned(threads));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <typename T>
+int run_forward(const WindowAttnParams& p, cudaStream_t s) {
+    return launch(window_fwd_kernel<T>, p, dim3(unsigned(p.n_t * p.B * p.hq)), kFwdThreads, kFwdSmem, s) == cudaSuccess
+               ? DUO_OK
+               : DUO_ERR_CUDA;
+}
+
+template <typename T>
+int run_backward(const WindowAttnParams& p, cudaStream_t s) {
+    const int64_t rows = int64_t(p.B) * p.hq * p.Tp;
+    if (launch(window_delta_kernel<T>, p, dim3(unsigned((rows + 15) / 16)), 256, 0, s) != cudaSuccess) return DUO_ERR_CUDA;
+    const unsigned items = unsigned(p.items_kv + p.n_t * p.B * p.hq);
+    if (launch(window_bwd_kernel<T>, p, dim3(items), kBwdThreads, kBwdSmem, s) != cudaSuccess) return DUO_ERR_CUDA;
+    const unsigned joins = unsigned(((p.p_long > 1 ? p.n_long : 0) + (p.p_short > 1 ? p.n_t - p.n_long : 0)) * p.B * p.n_kv);
+    if (joins > 0 && launch(window_join_kernel<T>, p, dim3(16 * joins), 256, 0, s) != cudaSuccess) return DUO_ERR_CUDA;
+    return DUO_OK;
+}
+
+}  // namespace
+
+}  // namespace duo
+
+extern "C" {
+
+int duo_window_attn_stats_bytes(const duo_window_attn_desc* d, size_t* bytes) {
+    const int rc = duo::check_desc(d);
+    if (rc) return rc;
+    if (!bytes) return DUO_ERR_INVALID_ARG;
+    *bytes = size_t(d->batch) * d->num_q_heads * duo::padded(d->tokens) * 4;
+    return DUO_OK;
+}
+
+int duo_window_attn_workspace_bytes(const duo_window_attn_desc* d, size_t* bytes) {
+    const int rc = duo::check_desc(d);
+    if (rc) return rc;
+    if (!bytes) return DUO_ERR_INVALID_ARG;
+    int sms = 0;
+    if (duo::device_sms(&sms)) return DUO_ERR_CUDA;
+    duo::WindowAttnParams p{};
+    duo::fill_params(p, *d, nullptr);
+    duo::plan_pieces(p, sms);
+    *bytes = duo::align256(size_t(d->batch) * d->num_q_heads * p.Tp * 4) +
+             size_t(duo::partial_slots(p)) * 2 * duo::kTile * duo::kTile * 4;
+    return DUO_OK;
+}
+
+int duo_window_attn(const duo_window_attn_desc* d, const duo_heads* q, const duo_heads* k, const duo_heads* v,
+                    const duo_heads* out, float* stats, int32_t* status, duo_stream_t stream) {
+    int rc = duo::check_desc(d);
+    if (rc) return rc;
+    if (d->batch == 0 || d->tokens == 0) return DUO_OK;
+    if (!stats) return DUO_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(stats) & 15) || (reinterpret_cast<uintptr_t>(status) & 3)) return DUO_ERR_ALIGNMENT;
+    for (const duo_heads* x : {q, k, v, out})
+        if ((rc = duo::check_heads(x, *d, x == k || x == v ? d->num_kv_heads : d->num_q_heads))) return rc;
+    int sms = 0;
+    if (duo::device_sms(&sms)) return DUO_ERR_CUDA;
+    duo::WindowAttnParams p{};
+    duo::fill_params(p, *d, status);
+    if (!duo::make_map(&p.tm_q, *q, *d, p.hq) || !duo::make_map(&p.tm_k, *k, *d, p.n_kv) ||
+        !duo::make_map(&p.tm_v, *v, *d, p.n_kv))
+        return DUO_ERR_CUDA;
+    p.out = duo::head_tensor(*out);
+    p.stats = stats;
+    return d->dtype == DUO_BF16 ? duo::run_forward<__nv_bfloat16>(p, stream) : duo::run_forward<__half>(p, stream);
+}
+
+int duo_window_attn_grad(const duo_window_attn_desc* d, const duo_heads* q, const duo_heads* k, const duo_heads* v,
+                         const duo_heads* out, const duo_heads* dout, const float* stats, const duo_heads* dq,
+                         const duo_heads* dk, const duo_heads* dv, void* workspace, size_t workspace_bytes,
+                         int32_t* status, duo_stream_t stream) {
+    int rc = duo::check_desc(d);
+    if (rc) return rc;
+    if (d->batch == 0 || d->tokens == 0) return DUO_OK;
+    if (!stats || !workspace) return DUO_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(stats) & 15) || (reinterpret_cast<uintptr_t>(status) & 3) ||
+        (reinterpret_cast<uintptr_t>(workspace) & 255))
+        return DUO_ERR_ALIGNMENT;
+    for (const duo_heads* x : {q, out, dout, dq})
+        if ((rc = duo::check_heads(x, *d, d->num_q_heads))) return rc;
+    for (const duo_heads* x : {k, v, dk, dv})
+        if ((rc = duo::check_heads(x, *d, d->num_kv_heads))) return rc;
+    size_t need = 0;
+    if ((rc = duo_window_attn_workspace_bytes(d, &need))) return rc;
+    if (workspace_bytes < need) return DUO_ERR_BUFFER_TOO_SMALL;
+    int sms = 0;
+    if (duo::device_sms(&sms)) return DUO_ERR_CUDA;
+    duo::WindowAttnParams p{};
+    duo::fill_params(p, *d, status);
+    duo::plan_pieces(p, sms);
+    if (!duo::make_map(&p.tm_q, *q, *d, p.hq) || !duo::make_map(&p.tm_k, *k, *d, p.n_kv) ||
+        !duo::make_map(&p.tm_v, *v, *d, p.n_kv) || !duo::make_map(&p.tm_do, *dout, *d, p.hq))
+        return DUO_ERR_CUDA;
+    p.out = duo::head_tensor(*out);
+    p.dout = duo::head_tensor(*dout);
+    p.dq = duo::head_tensor(*dq);
+    p.dk = duo::head_tensor(*dk);
+    p.dv = duo::head_tensor(*dv);
+    p.stats = const_cast<float*>(stats);
+    p.delta = static_cast<float*>(workspace);
+    p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) +
+                                      duo::align256(size_t(p.B) * p.hq * p.Tp * 4));
+    return d->dtype == DUO_BF16 ? duo::run_backward<__nv_bfloat16>(p, stream) : duo::run_backward<__half>(p, stream);
+}
+
+}  // extern "C"

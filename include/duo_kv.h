@@ -652,6 +652,69 @@ DUO_API int duo_kv_reserve(duo_kv* kv, const int32_t* len_before, const int32_t*
                            int32_t* len_after, int32_t* cu, int32_t* seq, int32_t* pos, int64_t* slot,
                            duo_stream_t stream);
 
+/* ------------------------------- attention with a window and sinks, for training */
+
+/* A tensor [batch][heads][tokens][128] by strides in elements (the 128
+ * elements of a head are contiguous); data and the strides of dimensions of
+ * more than one entry are multiples of 16 bytes, strides at least 128. */
+typedef struct {
+    void* data;
+    int64_t batch_stride;
+    int64_t head_stride;
+    int64_t token_stride;
+} duo_heads;
+
+/* Causal attention of whole sequences: row i sees the keys j <= i with
+ * j < sink or j > i - window; window = 0: every j <= i (sink is not used).
+ *   dtype: DUO_BF16 or DUO_FP16, of every tensor; head_dim 128;
+ *   scale > 0; num_q_heads a multiple of num_kv_heads (query head h reads
+ *   key head h * num_kv_heads / num_q_heads);
+ *   lengths: device int32 [batch] or NULL: tokens of each sequence (taken
+ *   into 0 .. tokens); what lies behind them is not read as a value (it may
+ *   hold anything), and results there are zero. */
+typedef struct {
+    int32_t dtype;
+    int32_t batch;
+    int32_t num_q_heads;
+    int32_t num_kv_heads;
+    int32_t head_dim;
+    int32_t tokens;
+    int32_t sink;
+    int32_t window;
+    float scale;
+    const int32_t* lengths;
+} duo_window_attn_desc;
+
+/* Bytes of the statistics that the forward leaves for the gradient. */
+DUO_API int duo_window_attn_stats_bytes(const duo_window_attn_desc* desc, size_t* bytes);
+
+/* Bytes of scratch that the gradient needs (on the current device). */
+DUO_API int duo_window_attn_workspace_bytes(const duo_window_attn_desc* desc, size_t* bytes);
+
+/* out = softmax(scale q k^T) v over the visible keys: the two branches of
+ * the gated forward that tells retrieval heads (window = 0) from streaming
+ * ones.  Products in the inputs' type with fp32 sums, softmax in fp32, one
+ * rounding of the result.
+ *   stats: device, duo_window_attn_stats_bytes, 16-byte aligned;
+ *   status: device int32 word or NULL: a pipeline wait that ran out sets
+ *     DUO_STATUS_WAIT_TIMEOUT there (the result then means nothing).
+ * Runs on the current device, which holds every tensor; out does not
+ * overlap the inputs. */
+DUO_API int duo_window_attn(const duo_window_attn_desc* desc, const duo_heads* q, const duo_heads* k,
+                            const duo_heads* v, const duo_heads* out, float* stats, int32_t* status,
+                            duo_stream_t stream);
+
+/* Gradients of q, k and v from that of out (dout), with the out and stats of
+ * the forward call: the sums over the query heads that share a key head
+ * included.  Deterministic: no atomics.  workspace: 256-byte aligned;
+ * BUFFER_TOO_SMALL below duo_window_attn_workspace_bytes.  Two calls that
+ * may run at once need two workspaces. */
+DUO_API int duo_window_attn_grad(const duo_window_attn_desc* desc, const duo_heads* q, const duo_heads* k,
+                                 const duo_heads* v, const duo_heads* out, const duo_heads* dout,
+                                 const float* stats, const duo_heads* dq, const duo_heads* dk,
+                                 const duo_heads* dv, void* workspace, size_t workspace_bytes, int32_t* status,
+                                 duo_stream_t stream);
+
 /* Override the number of CTAs the decode kernel splits the keys over
  * (0 = one persistent wave, the default).  For tests of split invariance;
  * the workspace requirement grows with it. */

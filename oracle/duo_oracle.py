@@ -533,3 +533,36 @@ class PageTables:
 
     def table(self):
         return np.array([p + [-1] * (self.most - len(p)) for p in self.pages], dtype=np.int32)
+
+
+# ------------------------------------------- attention of whole sequences, for training
+def window_visible(tokens, sink, window, length=None):
+    """[rows][keys] bool: row i sees j <= i with j < sink or j > i - window
+    (window 0: every j <= i); rows behind length see nothing."""
+    n = tokens if length is None else length
+    i, j = np.arange(tokens)[:, None], np.arange(tokens)[None]
+    sees = (j <= i) & (i < n)
+    return sees & ((j < sink) | (j > i - window)) if window else sees
+
+
+def window_attention(q, k, v, visible, scale):
+    """One head, fp64: (out, p), q [T][d], k, v [T][d].  What lies behind the
+    sequence is not looked at (its weights are 0 whatever it holds)."""
+    n = int(visible.any(1).sum())
+    q, k, v = (np.where(np.arange(len(x))[:, None] < n, x, 0.0) for x in (q, k, v))
+    s = np.where(visible, q @ k.T * scale, -np.inf)
+    top = np.where(visible.any(1), s.max(1), 0.0)
+    p = np.exp(s - top[:, None])
+    total = p.sum(1)
+    p = p / np.where(total > 0, total, 1.0)[:, None]
+    return p @ v, p
+
+
+def window_attention_grad(q, k, v, g, visible, scale):
+    """Gradients of one head's (q, k, v) from g, the gradient of out, by the
+    formulas of the softmax: dv = p^T g, ds = p (g v^T - rowsum(g out))."""
+    out, p = window_attention(q, k, v, visible, scale)
+    n = int(visible.any(1).sum())
+    q, k, v, g = (np.where(np.arange(len(x))[:, None] < n, x, 0.0) for x in (q, k, v, g))
+    ds = p * (g @ v.T - (g * out).sum(1, keepdims=True))
+    return scale * ds @ k, scale * ds.T @ q, p.T @ g

@@ -1,0 +1,309 @@
+"""Windowed attention and its gradient on the GPU against the fp64 oracle.
+
+Bounds, element by element, worked out in fp64 beside the reference.  u is
+half a step of the type (2^-8 for bf16, 2^-11 for fp16).
+
+* Scores: 128 exact products summed in fp32, at most 2^-23 of the sum of
+  magnitudes per addition, so es = scale 2^-16 max sum |q k|, and a softmax
+  weight is off by at most ep = 2 es + 2^-18 of itself (the fast exponential
+  2^-22 relative for arguments up to 2^4, the sum's roundings).
+* out: weights rounded once (u p), the result once (u |out|):
+    Eo = (u + ep) p|v| + u |out|.
+* dv: Ev = (u + ep) p^T|g| + u |dv|.
+* ds = p (g.v - D): D is the dot of g with the rounded out, so
+    Es = p (2^-16 |g|.|v| + |g|.Eo) + (u + ep) |ds|;
+  dq, dk: scale Es |k|, scale Es^T |q| (and 2^-16 of the magnitudes for the
+  fp32 sums), plus u of the result.
+fp16 has a smallest step: 2^-24 for each rounded weight, ds and result.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import duo_oracle as O
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+def _reference(q, k, v, g, sees, scale, dtype):
+    """(values, bounds) of (out, dq, dk, dv) for one head of fp64 arrays."""
+    u = torch.finfo(dtype).eps / 2
+    tiny = 2.0 ** -24 if dtype == torch.float16 else 0.0
+    n = int(sees.any(1).sum())
+    q, k, v, g = (np.where(np.arange(len(x))[:, None] < n, x, 0.0) for x in (q, k, v, g))
+    out, p = O.window_attention(q, k, v, sees, scale)
+    dq, dk, dv = O.window_attention_grad(q, k, v, g, sees, scale)
+    aq, ak, av, ag = (np.abs(x) for x in (q, k, v, g))
+    ep = 2 * scale * 2.0 ** -16 * float((aq @ ak.T).max()) + 2.0 ** -18
+    seen = sees.astype(np.float64)
+    eo = (u + ep) * (p @ av) + u * np.abs(out) + tiny * (1 + seen @ av)
+    ev = (u + ep) * (p.T @ ag) + u * np.abs(dv) + tiny * (1 + seen.T @ ag)
+    ds = p * (g @ v.T - (g * out).sum(1, keepdims=True))
+    es = p * (2.0 ** -16 * (ag @ av.T) + (ag * eo).sum(1, keepdims=True)) + (u + ep) * np.abs(ds) + tiny * seen
+    mag = 2.0 ** -16 * np.abs(ds)
+    eq = scale * (es + mag) @ ak + u * np.abs(dq) + tiny
+    ek = scale * (es + mag).T @ aq + u * np.abs(dk) + tiny
+    return (out, dq, dk, dv), (eo, eq, ek, ev)
+
+
+def _check(q, k, v, g, got, sink, window, lengths, scale, heads=None):
+    """got: (out, dq, dk, dv) tensors."""
+    B, hq, T, _ = q.shape
+    n_kv = k.shape[1]
+    G = hq // n_kv
+    x64 = [x.detach().double().cpu().numpy() for x in (q, k, v, g)]
+    res = [x.detach().double().cpu().numpy() for x in got]
+    assert all(np.isfinite(x).all() for x in res)
+    for b in range(B):
+        n = T if lengths is None else min(max(int(lengths[b]), 0), T)
+        sees = O.window_visible(T, sink, window or 0, n)
+        for kv in range(n_kv):
+            dk = dv = ek = ev = 0.0
+            for h in range(kv * G, kv * G + G):
+                (out, dq, a, c), (eo, eq, ea, ec) = _reference(x64[0][b, h], x64[1][b, kv], x64[2][b, kv], x64[3][b, h],
+                                                               sees, scale, q.dtype)
+                dk, dv, ek, ev = dk + a, dv + c, ek + ea, ev + ec
+                for name, y, ref, bound in (("out", res[0], out, eo), ("dq", res[1], dq, eq)):
+                    _within(f"{name} b{b} h{h}", y[b, h], ref, bound, n)
+            for name, y, ref, bound in (("dk", res[2], dk, ek), ("dv", res[3], dv, ev)):
+                _within(f"{name} b{b} kv{kv}", y[b, kv], ref, bound, n)
+
+
+def _within(name, y, ref, bound, n):
+    assert not y[n:].any(), f"{name}: not zero behind the sequence"
+    err = np.abs(y - ref)
+    worst = (err / np.maximum(bound, 1e-30))[err > 0].max() if (err > 0).any() else 0.0
+    assert worst <= 1.0, f"{name}: {worst:.3g} bounds at {np.unravel_index((err - bound).argmax(), err.shape)}"
+
+
+def _make(B, hq, n_kv, T, dtype, token_major, seed):
+    gen = torch.Generator().manual_seed(seed)
+    out = []
+    for h in (hq, n_kv, n_kv, hq):
+        x = torch.randn(*((B, T, h) if token_major else (B, h, T)), 128, generator=gen).to(dtype).to(DEV)
+        out.append(x.transpose(1, 2) if token_major else x)
+    return out
+
+
+def _run(q, k, v, g, sink, window, lengths=None, scale=None):
+    from head_wise_kv_b200 import window_attention
+    x = [t.detach().requires_grad_() for t in (q, k, v)]
+    le = torch.tensor(lengths, dtype=torch.int32, device=DEV) if lengths is not None else None
+    out = window_attention(*x, sink, window, lengths=le, scale=scale)
+    return (out, *torch.autograd.grad(out, x, g))
+
+
+CASES = [   # B, hq, n_kv, T, sink, window, lengths
+    (1, 1, 1, 1, 0, None, None), (2, 2, 1, 1, 3, 1, [0, 1]), (1, 2, 2, 127, 0, 1, None), (1, 2, 1, 128, 4, 16, None),
+    (2, 4, 2, 129, 0, None, None), (2, 4, 4, 257, 16, 64, [257, 129]), (3, 2, 1, 300, 4, 33, [0, 1, 128]),
+    (1, 3, 1, 511, 0, 128, [400]), (1, 8, 1, 700, 64, 256, None), (1, 2, 1, 901, 200, 33, [-5]),
+    (1, 2, 1, 901, 200, 33, [5000]), (1, 2, 2, 640, 0, None, [555]), (1, 1, 1, 640, 5000, 7, None),
+    (2, 2, 1, 385, 0, 5000, None), (1, 1, 1, 1500, 130, 400, None),
+]
+
+
+@pytest.mark.parametrize("B,hq,n_kv,T,sink,window,lengths", CASES)
+@pytest.mark.parametrize("dtype,token_major", [(torch.bfloat16, True), (torch.float16, False)])
+def test_values_and_gradients(B, hq, n_kv, T, sink, window, lengths, dtype, token_major):
+    from head_wise_kv_b200 import window_attention_status
+    q, k, v, g = _make(B, hq, n_kv, T, dtype, token_major, T)
+    got = _run(q, k, v, g, sink, window, lengths)
+    assert window_attention_status(DEV) == 0
+    assert [t.stride() for t in got] == [t.stride() for t in (q, q, k, v)] or T == 1 or B == 1 or 1 in (hq, n_kv)
+    _check(q, k, v, g, got, sink, window, lengths, 128 ** -0.5)
+
+
+def _marks(B, h, T, scale=1.0):
+    """Row j holds `scale` at element j mod 128: a sum over tokens keeps those of every residue apart."""
+    x = torch.zeros(B, h, T, 128, dtype=torch.bfloat16, device=DEV)
+    t = torch.arange(T, device=DEV)
+    x[:, :, t, t % 128] = scale
+    return x
+
+
+@pytest.mark.parametrize("T,sink,window", [(385, 0, None), (700, 64, 256), (901, 200, 33), (1100, 130, 128), (600, 0, 129),
+                                           (640, 1, 1)])
+def test_every_pair_counts_once(T, sink, window):
+    """Uniform weights and marked tokens: one pair too many or too few moves a sum of at most T / 128 + 1 terms."""
+    q, k, v, g = _make(1, 2, 1, T, torch.bfloat16, False, 3)
+    marks_q, marks_kv = _marks(1, 2, T), _marks(1, 1, T)
+    for x in ((torch.zeros_like(q), marks_kv, marks_kv, g), (marks_q, torch.zeros_like(k), v, marks_q),
+              (torch.zeros_like(q), marks_kv, v, marks_q)):
+        _check(*x, _run(*x, sink, window), sink, window, None, 128 ** -0.5)
+
+
+@pytest.mark.parametrize("hq,n_kv,T,sink,window", [(8, 1, 2200, 64, 256), (4, 2, 2050, 0, None), (16, 1, 1300, 300, 200)])
+def test_key_tiles_in_pieces(hq, n_kv, T, sink, window):
+    """Few key heads and many rows: the lists of the key tiles are shared out and joined."""
+    q, k, v, g = _make(1, hq, n_kv, T, torch.bfloat16, True, 5)
+    _check(q, k, v, g, _run(q, k, v, g, sink, window, [T - 3]), sink, window, [T - 3], 128 ** -0.5)
+
+
+def test_what_lies_behind_a_sequence_does_not_matter():
+    B, T = 3, 300
+    lengths = [300, 131, 0]
+    q, k, v, g = _make(B, 4, 2, T, torch.bfloat16, True, 8)
+    for window in (None, 40):
+        clean = _run(q, k, v, g, 4, window, lengths)
+        bad = [x.clone() for x in (q, k, v, g)]
+        for i, x in enumerate(bad):
+            for b, n in enumerate(lengths):
+                x[b, :, n:] = (float("nan"), float("inf"), float("-inf"), float("nan"))[i]
+        assert all(torch.equal(a, b) for a, b in zip(clean, _run(*bad, 4, window, lengths)))
+
+
+def test_large_scores_and_a_given_scale():
+    q, k, v, g = _make(1, 2, 1, 260, torch.bfloat16, False, 9)
+    q = q * 30          # weights close to one-hot, maxima that grow along the row
+    got = _run(q, k, v, g, 2, 70, scale=0.125)
+    _check(q, k, v, g, got, 2, 70, None, 0.125)
+
+
+def test_views_expanded_and_misaligned_inputs():
+    from head_wise_kv_b200 import window_attention
+    B, T, hq, n_kv = 2, 150, 4, 2
+    gen = torch.Generator().manual_seed(10)
+    qkv = torch.randn(B, T, hq + 2 * n_kv, 128, generator=gen).to(torch.bfloat16).to(DEV).requires_grad_()
+    g = torch.randn(B, T, hq, 128, generator=gen).to(torch.bfloat16).to(DEV).transpose(1, 2)
+    q, k, v = (t.transpose(1, 2) for t in qkv.split([hq, n_kv, n_kv], 2))       # parts of one projection
+    out = window_attention(q, k, v, 4, 30)
+    grad, = torch.autograd.grad(out, qkv, g)
+    grads = [t.transpose(1, 2) for t in grad.split([hq, n_kv, n_kv], 2)]
+    _check(q, k, v, g, (out, *grads), 4, 30, None, 128 ** -0.5)
+    # one sequence's keys for the whole batch (the gradient adds up), and a gradient of a sum (expanded)
+    k1, v1 = (t[:1].detach().contiguous().requires_grad_() for t in (k, v))
+    out = window_attention(q.detach(), k1.expand(B, -1, -1, -1), v1.expand(B, -1, -1, -1), 4, 30)
+    gk, gv = torch.autograd.grad(out.sum(), (k1, v1))
+    ones = torch.ones_like(out)
+    want = _run(q, k1.expand(B, -1, -1, -1).contiguous(), v1.expand(B, -1, -1, -1).contiguous(), ones, 4, 30)
+    assert torch.equal(out, want[0])
+    for a, b in ((gk, want[2]), (gv, want[3])):
+        assert torch.equal(a, b.sum(0, keepdim=True))
+    # storage that no 16-byte load may start at, and heads that are not contiguous
+    pad = torch.randn(B, hq, T, 132, generator=gen).to(torch.bfloat16).to(DEV)[..., 2:130]
+    flip = torch.randn(B, hq, 128, T, generator=gen).to(torch.bfloat16).to(DEV).transpose(2, 3)
+    for x in (pad, flip):
+        assert torch.equal(window_attention(x, k, v, 4, 30), window_attention(x.contiguous(), k, v, 4, 30))
+
+
+def test_gradients_only_where_asked_and_no_grad():
+    from head_wise_kv_b200 import window_attention
+    q, k, v, g = _make(1, 2, 1, 140, torch.bfloat16, False, 12)
+    want = _run(q, k, v, g, 0, None)
+    kk = k.clone().requires_grad_()
+    out = window_attention(q, kk, v)
+    out.backward(g)
+    assert torch.equal(kk.grad, want[2]) and torch.equal(out, want[0])
+    assert not window_attention(q, k, v).requires_grad
+
+
+def test_differences():
+    """The gradient along a direction against the oracle's difference of the loss."""
+    T, scale, h = 200, 128 ** -0.5, 2.0 ** -12
+    q, k, v, g = _make(1, 1, 1, T, torch.bfloat16, False, 13)
+    got = _run(q, k, v, g, 4, 50)
+    x64 = [x[0, 0].double().cpu().numpy() for x in (q, k, v)]
+    g64 = g[0, 0].double().cpu().numpy()
+    sees = O.window_visible(T, 4, 50)
+    _, bounds = _reference(*x64, g64, sees, scale, torch.bfloat16)
+    rng = np.random.default_rng(0)
+    for i in range(3):
+        u = rng.standard_normal((T, 128))
+        f = [(O.window_attention(*[x + s * h * u if j == i else x for j, x in enumerate(x64)], sees, scale)[0] * g64).sum()
+             for s in (1, -1)]
+        slope = (got[1 + i][0, 0].double().cpu().numpy() * u).sum()
+        # the bounds of the gradient, and h^2 / 6 times a third derivative below 2^16
+        assert abs((f[0] - f[1]) / (2 * h) - slope) <= (bounds[1 + i] * np.abs(u)).sum() + h * h / 6 * 2 ** 16
+
+
+def test_same_bits_again_on_another_stream_and_in_a_graph():
+    from head_wise_kv_b200 import window_attention
+    q, k, v, g = _make(2, 8, 2, 700, torch.bfloat16, True, 14)
+    want = _run(q, k, v, g, 64, 128)
+    assert all(torch.equal(a, b) for a, b in zip(want, _run(q, k, v, g, 64, 128)))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = _run(q, k, v, g, 64, 128)
+    torch.cuda.current_stream().wait_stream(side)
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    # forward and backward captured together, with leaves of the capture's own, replayed on new inputs
+    x = [t.detach().clone().requires_grad_() for t in (q, k, v)]
+    gg = g.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = window_attention(*x, 64, 128)
+        res = (out, *torch.autograd.grad(out, x, gg))
+    for seed in (15, 16):
+        new = _make(2, 8, 2, 700, torch.bfloat16, True, seed)
+        with torch.no_grad():
+            for a, b in zip((*x, gg), new):
+                a.copy_(b)
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(res, _run(*new, 64, 128)))
+
+
+def test_empty_and_refusals():
+    from head_wise_kv_b200 import window_attention, window_attention_status
+    q, k, v, g = _make(2, 4, 2, 20, torch.bfloat16, False, 17)
+    assert window_attention(q[:0], k[:0], v[:0]).shape == (0, 4, 20, 128)
+    got = _run(q[:, :, :0], k[:, :, :0], v[:, :, :0], g[:, :, :0], 0, 3)
+    assert [t.shape[2] for t in got] == [0, 0, 0, 0]
+    le = torch.zeros(2, dtype=torch.int32, device=DEV)
+    for bad in (lambda: window_attention(q, k[:, :, :10], v), lambda: window_attention(q, k, v[:, :1]),
+                lambda: window_attention(q[:, :3], k, v), lambda: window_attention(q[0], k, v),
+                lambda: window_attention(q, k, v, -1), lambda: window_attention(q, k, v, 0, 0),
+                lambda: window_attention(q, k, v, lengths=le[:1]), lambda: window_attention(q, k, v, lengths=le.cpu()),
+                lambda: window_attention(q, k, v, lengths=le.long()), lambda: window_attention(q, k, v, scale=0.0),
+                lambda: window_attention(q[..., :64], k[..., :64], v[..., :64]), lambda: window_attention(q, k.cpu(), v)):
+        with pytest.raises(ValueError):
+            bad()
+    for bad in (lambda: window_attention(q.float(), k.float(), v.float()), lambda: window_attention(q, k.half(), v)):
+        with pytest.raises(TypeError):
+            bad()
+    assert window_attention_status(DEV) == 0
+
+
+def test_gated_branches_with_rotary_positions():
+    """The layer in which heads are told apart: rotate, both branches, gate; gradients of the projection and the gate."""
+    from head_wise_kv_b200 import Rope, window_attention
+    B, T, hq, n_kv, S, W = 2, 260, 4, 2, 8, 48
+    gen = torch.Generator().manual_seed(20)
+    qkv = torch.randn(B, T, hq + 2 * n_kv, 128, generator=gen).to(torch.bfloat16).to(DEV).requires_grad_()
+    alpha = torch.rand(hq, generator=gen).to(DEV).requires_grad_()
+    w = torch.randn(B, hq, T, 128, generator=gen).to(DEV)
+    rope = Rope(128)
+    pos = torch.zeros(B, dtype=torch.int32, device=DEV)
+    q, k, v = (t.transpose(1, 2) for t in qkv.split([hq, n_kv, n_kv], 2))
+    q, k = rope.apply(q, pos), rope.apply(k, pos)
+    gate = alpha[None, :, None, None]
+    full, stream = window_attention(q, k, v), window_attention(q, k, v, S, W)
+    loss = ((gate * full.float() + (1 - gate) * stream.float()) * w).sum()
+    g_qkv, g_alpha = torch.autograd.grad(loss, (qkv, alpha))
+    # the same in fp64, from the definition
+    x = qkv.detach().double().requires_grad_()
+    a64 = alpha.detach().double().requires_grad_()
+    f, _ = rope.frequencies()
+    ang = torch.arange(T, device=DEV).double()[:, None] * torch.tensor(f, dtype=torch.float64, device=DEV)
+
+    def turn(t):
+        y, z = t[..., :64], t[..., 64:]
+        return torch.cat([y * ang.cos() - z * ang.sin(), z * ang.cos() + y * ang.sin()], -1)
+    qd, kd, vd = (t.transpose(1, 2) for t in x.split([hq, n_kv, n_kv], 2))
+    qd, kd = turn(qd), turn(kd).repeat_interleave(hq // n_kv, 1)
+    vd = vd.repeat_interleave(hq // n_kv, 1)
+
+    def branch(s, win):
+        sees = torch.from_numpy(O.window_visible(T, s, win)).to(DEV)
+        return torch.softmax((qd @ kd.transpose(2, 3) * 128 ** -0.5).masked_fill(~sees, -torch.inf), -1) @ vd
+    g64 = a64[None, :, None, None]
+    ref = ((g64 * branch(0, 0) + (1 - g64) * branch(S, W)) * w.double()).sum()
+    r_qkv, r_alpha = torch.autograd.grad(ref, (x, a64))
+    # a chain of four bf16 roundings on each path (rotated input, weights, ds or branch, result) and the backward's
+    # rotation: rms 2^-8 / sqrt(3) each, independent, at most eight of them
+    rel = float((g_qkv.double() - r_qkv).norm() / r_qkv.norm())
+    assert rel <= 2.0 ** -8 * (8 / 3) ** 0.5, rel
+    # the gate's gradient: 2 T B 128 terms |w| |branch| with errors of rms 2^-8 of the branches' size
+    scale = float((w.double() ** 2 * (branch(0, 0).detach() ** 2 + branch(S, W).detach() ** 2)).sum((0, 2, 3)).sqrt().max())
+    assert float((g_alpha.double() - r_alpha).abs().max()) <= 4 * 2.0 ** -8 * scale
