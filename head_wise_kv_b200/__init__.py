@@ -5,8 +5,9 @@ thin Python binding.
 ``DuoKVCache`` owns the cache as a torch buffer and calls the library;
 ``Rope`` rotates queries and keys, ``TokenMap`` holds a step's token map;
 ``window_attention`` is the differentiable attention of whole sequences;
-``_lib`` exposes the C functions one to one.  Both load libduo_kv.so on first
-use and raise ImportError if it is missing (build it with
+``_lib`` exposes the C functions one to one.  All load libduo_kv.so (and the
+compiled half of the binding, _binding.so) on first use and raise ImportError
+if one is missing (build both with
 ``python -m head_wise_kv_b200.build``); there is no fallback path.
 """
 __all__ = ["DuoKVCache", "DuoError", "Rope", "TokenMap", "window_attention", "window_attention_status"]

@@ -1,4 +1,5 @@
-"""Build libduo_kv.so in-tree for sm_100a with nvcc.
+"""Build libduo_kv.so in-tree for sm_100a with nvcc, and the compiled half of
+the Python binding (_binding.so) with g++ against torch's headers.
 
     python -m head_wise_kv_b200.build          # incremental
     python -m head_wise_kv_b200.build --force  # rebuild everything
@@ -17,6 +18,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJDIR = os.path.join(ROOT, "_build", "duo_kv")
 LIB = os.path.join(PKG, "libduo_kv.so")
+BINDING_SRC = os.path.join(CSRC, "bindings.cpp")
+BINDING = os.path.join(PKG, "_binding.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -62,7 +65,31 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
         if verbose:
             print(" ".join(cmd), flush=True)
         subprocess.run(cmd, check=True)
+    build_binding(force, verbose)
     return LIB
+
+
+def build_binding(force: bool = False, verbose: bool = False) -> str:
+    """_binding.so: links libduo_kv.so beside it and the torch that is installed."""
+    inputs = [BINDING_SRC, os.path.join(INCLUDE, "duo_kv.h")]
+    if not force and os.path.exists(BINDING) and all(os.path.getmtime(BINDING) >= os.path.getmtime(f) for f in inputs):
+        return BINDING
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    home = os.path.dirname(os.path.dirname(nvcc()))
+    libs = cpp_extension.library_paths()
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-DTORCH_EXTENSION_NAME=_binding",
+           "-DTORCH_API_INCLUDE_EXTENSION_H", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f"-I{INCLUDE}", *[f"-isystem{d}" for d in cpp_extension.include_paths()],
+           f"-isystem{sysconfig.get_path('include')}", f"-isystem{home}/include", BINDING_SRC, "-o", BINDING,
+           *[f"-L{d}" for d in libs], "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python",
+           f"-L{PKG}", "-l:libduo_kv.so", "-Wl,-rpath,$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    return BINDING
 
 
 def main(argv=None):

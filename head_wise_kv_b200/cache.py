@@ -8,6 +8,7 @@ import numpy as np
 import torch
 
 from . import _lib as L
+from . import _binding as _b
 
 
 def _stream(device) -> int:
@@ -42,24 +43,6 @@ def _need(t: torch.Tensor, name: str, dtype, shape, device):
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
-
-
-def _rows(t, name, heads, d, lead, device):
-    """A projection's rows [lead...][heads][d], bf16, token-major: duo_rows."""
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name}: dtype {t.dtype}, expected {torch.bfloat16}")
-    if tuple(t.shape) != (*lead, heads, d):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(*lead, heads, d)}")
-    if t.device != device:
-        raise ValueError(f"{name}: on {t.device}, expected {device}")
-    s = t.stride()
-    if s[-1] != 1:
-        raise ValueError(f"{name}: the elements of a head must be contiguous")
-    if len(lead) == 2 and lead[0] > 1 and lead[1] > 1 and s[0] != lead[1] * s[1]:
-        raise ValueError(f"{name}: sequences must follow one another at the token stride")
-    token = s[0] if len(lead) == 1 or lead[1] == 1 else s[1]
-    # a dimension of one row has no stride that matters
-    return L.duo_rows(t.data_ptr(), token if t.numel() > heads * d else 0, s[-2] if heads > 1 else 0)
 
 
 class TokenMap:
@@ -129,6 +112,7 @@ class DuoKVCache:
         with torch.cuda.device(self.device):
             self.buf = torch.empty(self.total_bytes, dtype=torch.uint8, device=self.device)
             self.handle = L.duo_kv_alloc(self._desc, self.buf.data_ptr(), self.total_bytes, _stream(self.device))
+        self._calls = _b.Cache(self.handle, self.device.index, self.B, self.hq, self.n_kv, self.d)
         self._ws = None
         self._alloc_workspace()
 
@@ -177,21 +161,7 @@ class DuoKVCache:
         step's tokens in ``tokens`` (a TokenMap, returned); see
         duo_kv_reserve.  Without ``tokens`` only the pages are reserved and
         len_after (int32 [batch]) is returned."""
-        bp = _need(len_before, "len_before", torch.int32, (self.B,), self.device)
-        np_ = _need(n_new, "n_new", torch.int32, (self.B,), self.device) if n_new is not None else None
-        if tokens is None:
-            after = torch.empty(self.B, dtype=torch.int32, device=self.device)
-            with _on(self.device):
-                L.duo_kv_reserve(self.handle, bp, np_, 0, after.data_ptr(), None, None, None, None,
-                                 _stream(self.device))
-            return after
-        if tokens.batch != self.B or tokens.device != self.device:
-            raise ValueError("the token map is of another batch or device")
-        with _on(self.device):
-            L.duo_kv_reserve(self.handle, bp, np_, tokens.max_tokens, tokens.len_after.data_ptr(),
-                             tokens.cu.data_ptr(), tokens.seq.data_ptr(), tokens.pos.data_ptr(),
-                             tokens.slot.data_ptr(), _stream(self.device))
-        return tokens
+        return self._calls.reserve(len_before, n_new, tokens)
 
     def fork(self, src: int, dst: int, length: int):
         """Sequence dst continues from the first ``length`` tokens of
@@ -211,6 +181,7 @@ class DuoKVCache:
         if getattr(self, "handle", None):
             L.duo_kv_free(self.handle)
             self.handle = None
+            self._calls = _b.Cache(0, self.device.index, self.B, self.hq, self.n_kv, self.d)
 
     def __del__(self):
         try:
@@ -344,36 +315,7 @@ class DuoKVCache:
         q may be None (keys and values only).  Returns the rotated queries
         (contiguous, in ``out`` if given; rows without a token stay as they
         were, zero where out is new)."""
-        if rope.d != self.d:
-            raise ValueError(f"rope of head_dim {rope.d}, expected {self.d}")
-        lead = (tokens.max_tokens,) if tokens is not None else tuple(k.shape[:2])
-        if tokens is None and (len(lead) != 2 or k.dim() != 4 or lead[0] != self.B):
-            raise ValueError(f"a padded batch is [{self.B}][tokens][heads][{self.d}]")
-        bp = _need(len_before, "len_before", torch.int32, (self.B,), self.device)
-        tmap = np_ = qr = op = None
-        if tokens is not None:
-            if n_new is not None:
-                raise ValueError("n_new belongs to a padded batch: the token map says how many tokens there are")
-            if tokens.batch != self.B or tokens.device != self.device:
-                raise ValueError("the token map is of another batch or device")
-            tmap = L.duo_token_map(tokens.seq.data_ptr(), tokens.pos.data_ptr(), tokens.slot.data_ptr(),
-                                   tokens.len_after.data_ptr())
-        elif n_new is not None:
-            np_ = _need(n_new, "n_new", torch.int32, (self.B,), self.device)
-        kr = _rows(k, "k", self.n_kv, self.d, lead, self.device)
-        vr = _rows(v, "v", self.n_kv, self.d, lead, self.device)
-        if q is not None:
-            qr = _rows(q, "q", self.hq, self.d, lead, self.device)
-            if out is None:
-                make = torch.empty if tokens is None and n_new is None else torch.zeros
-                out = make(*lead, self.hq, self.d, dtype=torch.bfloat16, device=self.device)
-            op = _need(out, "out", torch.bfloat16, (*lead, self.hq, self.d), self.device)
-        elif out is not None:
-            raise ValueError("out without q")
-        with _on(self.device):
-            L.duo_kv_append_rope(self.handle, layer, rope.handle, qr, kr, vr, bp, tmap, np_, lead[-1], op,
-                                 _stream(self.device))
-        return out
+        return self._calls.append_rope(layer, rope.handle or 0, rope.d, q, k, v, len_before, tokens, n_new, out)
 
     def step_rope(self, layer: int, rope, q, k, v, len_before, lengths, scale: float, out=None, lse=None,
                   want_lse=False, q_rot=None):
@@ -383,26 +325,8 @@ class DuoKVCache:
         len_before + 1); see duo_decode_step_rope.  q_rot: bf16 [B][Hq][d]
         scratch for the rotated queries (allocated if not given).  Returns
         fp32 out [B][Hq][d] (and lse [B][Hq] if asked)."""
-        if rope.d != self.d:
-            raise ValueError(f"rope of head_dim {rope.d}, expected {self.d}")
-        qr = _rows(q, "q", self.hq, self.d, (self.B,), self.device)
-        kr = _rows(k, "k", self.n_kv, self.d, (self.B,), self.device)
-        vr = _rows(v, "v", self.n_kv, self.d, (self.B,), self.device)
-        bp = _need(len_before, "len_before", torch.int32, (self.B,), self.device)
-        lp = _need(lengths, "lengths", torch.int32, (self.B,), self.device)
-        if q_rot is None:
-            q_rot = torch.empty(self.B, self.hq, self.d, dtype=torch.bfloat16, device=self.device)
-        rp = _need(q_rot, "q_rot", torch.bfloat16, (self.B, self.hq, self.d), self.device)
-        if out is None:
-            out = torch.empty(self.B, self.hq, self.d, dtype=torch.float32, device=self.device)
-        op = _need(out, "out", torch.float32, (self.B, self.hq, self.d), self.device)
-        if want_lse and lse is None:
-            lse = torch.empty(self.B, self.hq, dtype=torch.float32, device=self.device)
-        sp = _need(lse, "lse", torch.float32, (self.B, self.hq), self.device) if lse is not None else None
-        with _on(self.device):
-            L.duo_decode_step_rope(self.handle, layer, rope.handle, qr, kr, vr, bp, lp, float(scale), rp, op, sp,
-                                   self._ws.data_ptr(), self._ws.numel(), _stream(self.device))
-        return (out, lse) if lse is not None else out
+        return self._calls.step_rope(layer, rope.handle or 0, rope.d, q, k, v, len_before, lengths, float(scale), out,
+                                     lse, want_lse, q_rot, self._ws)
 
     def prefill_rope(self, layer: int, rope, q, k, v, prefix_len, scale: float, n_new=None, out=None):
         """A prompt chunk of one layer from the projections' rows (bf16 q

@@ -1,0 +1,449 @@
+// Compiled half of the Python binding: the calls that a program makes once
+// per layer and step, with their checks of shapes, types and devices, and the
+// autograd function of the windowed attention.  A decode step's kernels run
+// for a few microseconds; the same checks and conversions in Python and
+// ctypes cost more than that (8 to 15 us a call, 200 us for a small
+// attention's forward and backward).  Nothing is computed here: every step of
+// the path runs in the library's kernels (duo_kv.h).
+#include <ATen/core/grad_mode.h>
+#include <c10/cuda/CUDAGuard.h>
+#include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/autograd/functions/basic_ops.h>
+#include <torch/extension.h>
+
+#include <limits>
+#include <mutex>
+#include <optional>
+#include <sstream>
+#include <stdexcept>
+#include <string>
+#include <vector>
+
+#include "duo_kv.h"
+
+namespace py = pybind11;
+
+namespace {
+
+using at::Tensor;
+using OptTensor = std::optional<Tensor>;
+
+// An error code of the library; Python sees _lib.DuoError.
+struct DuoFailure : std::runtime_error {
+    int code;
+    std::string what_call;
+    DuoFailure(int c, const char* call)
+        : std::runtime_error(std::string(call) + ": " + duo_strerror(c)), code(c), what_call(call) {}
+};
+
+void check(int code, const char* call) {
+    if (code != DUO_OK) throw DuoFailure(code, call);
+}
+
+std::string shape_of(at::IntArrayRef s) {
+    std::ostringstream o;
+    o << '(';
+    for (size_t i = 0; i < s.size(); ++i) o << (i ? ", " : "") << s[i];
+    o << ')';
+    return o.str();
+}
+
+// A contiguous tensor of one type, shape and device.
+void need(const Tensor& t, const char* name, at::ScalarType type, at::IntArrayRef shape, const at::Device& dev) {
+    TORCH_CHECK_TYPE(t.scalar_type() == type, name, ": dtype ", t.scalar_type(), ", expected ", type);
+    TORCH_CHECK_VALUE(t.sizes() == shape, name, ": shape ", shape_of(t.sizes()), ", expected ", shape_of(shape));
+    TORCH_CHECK_VALUE(t.device() == dev, name, ": on ", t.device(), ", expected ", dev);
+    TORCH_CHECK_VALUE(t.is_contiguous(), name, " must be contiguous");
+}
+
+const int32_t* ints(const Tensor& t) { return static_cast<const int32_t*>(t.data_ptr()); }
+const int32_t* ints(const OptTensor& t) { return t ? ints(*t) : nullptr; }
+
+cudaStream_t stream_of(const at::Device& dev) { return c10::cuda::getCurrentCUDAStream(dev.index()).stream(); }
+
+// ------------------------------------------------------------------ rotary positions
+int rope_dtype(at::ScalarType t) {
+    switch (t) {
+        case at::kBFloat16: return DUO_BF16;
+        case at::kHalf: return DUO_FP16;
+        case at::kFloat: return DUO_FP32;
+        default: return -1;
+    }
+}
+
+Tensor rope_apply(uintptr_t plan, int64_t d, const Tensor& x, const Tensor& positions, const OptTensor& n_new,
+                  bool transpose, const OptTensor& given) {
+    const int dtype = rope_dtype(x.scalar_type());
+    TORCH_CHECK_TYPE(dtype >= 0, "dtype ", x.scalar_type(), ", expected bfloat16, float16 or float32");
+    const at::Device dev = x.device();
+    TORCH_CHECK_VALUE(dev.is_cuda(), "the tensors must be on a CUDA device");
+    TORCH_CHECK_VALUE(x.dim() == 4 && x.size(3) == d, "shape ", shape_of(x.sizes()), ", expected [batch][heads][tokens][", d,
+                      "]");
+    const int64_t B = x.size(0), H = x.size(1), n = x.size(2);
+    const bool per_token = positions.dim() == 2;
+    TORCH_CHECK_VALUE(positions.scalar_type() == at::kInt && positions.device() == dev && positions.is_contiguous(),
+                      "positions must be contiguous int32 on the tensors' device");
+    TORCH_CHECK_VALUE(per_token ? positions.sizes() == at::IntArrayRef({B, n}) : positions.sizes() == at::IntArrayRef({B}),
+                      "positions: shape ", shape_of(positions.sizes()), ", expected (", B, ",) or (", B, ", ", n, ")");
+    if (n_new)
+        TORCH_CHECK_VALUE(n_new->scalar_type() == at::kInt && n_new->device() == dev && n_new->is_contiguous() &&
+                              n_new->sizes() == at::IntArrayRef({B}),
+                          "n_new must be contiguous int32 [", B, "] on the tensors' device");
+    const c10::cuda::CUDAGuard guard(dev);
+    Tensor out;
+    if (given) {
+        out = *given;
+        TORCH_CHECK_VALUE(out.sizes() == x.sizes() && out.scalar_type() == x.scalar_type() && out.device() == dev,
+                          "out must have the input's shape, dtype and device");
+    } else {
+        out = n_new ? at::zeros(x.sizes(), x.options()) : at::empty(x.sizes(), x.options());
+    }
+    TORCH_CHECK_VALUE(x.stride(3) == 1 && out.stride(3) == 1, "the elements of a head must be contiguous");
+    duo_rope_tensor t{};
+    t.in = x.data_ptr();
+    t.out = out.data_ptr();
+    t.heads = int32_t(H);
+    t.rotate = 1;
+    TORCH_CHECK_VALUE(H >= 1 || B * n == 0, "a tensor has at least one head");
+    for (int i = 0; i < 3; ++i) {     // a dimension of one entry has no stride that matters
+        t.in_stride[i] = x.size(i) > 1 ? x.stride(i) : 0;
+        t.out_stride[i] = x.size(i) > 1 ? out.stride(i) : 0;
+    }
+    if (x.numel() == 0) return out;
+    check(duo_rope_apply(reinterpret_cast<const duo_rope*>(plan), dtype, transpose, int32_t(B), int32_t(n), &t, 1,
+                         ints(positions), per_token, ints(n_new), stream_of(dev)),
+          "duo_rope_apply");
+    return out;
+}
+
+// ------------------------------------------------------------------ the cache's calls
+// A projection's rows [lead...][heads][d], bf16, token-major.
+duo_rows rows_of(const Tensor& t, const char* name, int64_t heads, int64_t d, at::IntArrayRef lead, const at::Device& dev) {
+    TORCH_CHECK_TYPE(t.scalar_type() == at::kBFloat16, name, ": dtype ", t.scalar_type(), ", expected ", at::kBFloat16);
+    const size_t n = lead.size();
+    bool same = size_t(t.dim()) == n + 2 && t.size(n) == heads && t.size(n + 1) == d;
+    for (size_t i = 0; same && i < n; ++i) same = t.size(i) == lead[i];
+    TORCH_CHECK_VALUE(same, name, ": shape ", shape_of(t.sizes()), ", expected ", shape_of(lead), " x (", heads, ", ", d, ")");
+    TORCH_CHECK_VALUE(t.device() == dev, name, ": on ", t.device(), ", expected ", dev);
+    TORCH_CHECK_VALUE(t.stride(n + 1) == 1, name, ": the elements of a head must be contiguous");
+    TORCH_CHECK_VALUE(n == 1 || lead[0] <= 1 || lead[1] <= 1 || t.stride(0) == lead[1] * t.stride(1), name,
+                      ": sequences must follow one another at the token stride");
+    const int64_t token = n == 1 || lead[1] == 1 ? t.stride(0) : t.stride(1);
+    // a dimension of one row has no stride that matters
+    return duo_rows{static_cast<const uint16_t*>(t.data_ptr()), t.numel() > heads * d ? token : 0,
+                    heads > 1 ? t.stride(n) : 0};
+}
+
+struct Cache {
+    duo_kv* kv;
+    at::Device dev;
+    int64_t B, hq, n_kv, d;
+
+    Cache(uintptr_t handle, int64_t device, int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t head_dim)
+        : kv(reinterpret_cast<duo_kv*>(handle)),
+          dev(at::kCUDA, at::DeviceIndex(device)),
+          B(batch),
+          hq(q_heads),
+          n_kv(kv_heads),
+          d(head_dim) {}
+
+    OptTensor append_rope(int64_t layer, uintptr_t rope, int64_t rope_d, const OptTensor& q, const Tensor& k, const Tensor& v,
+                          const Tensor& len_before, const py::object& tokens, const OptTensor& n_new,
+                          const OptTensor& given) const {
+        TORCH_CHECK_VALUE(rope_d == d, "rope of head_dim ", rope_d, ", expected ", d);
+        duo_token_map map{};
+        const bool ragged = !tokens.is_none();
+        std::vector<int64_t> lead;
+        Tensor seq, pos, slot, after;
+        if (ragged) {
+            TORCH_CHECK_VALUE(!n_new, "n_new belongs to a padded batch: the token map says how many tokens there are");
+            const int64_t T = tokens.attr("max_tokens").cast<int64_t>();
+            TORCH_CHECK_VALUE(tokens.attr("batch").cast<int64_t>() == B, "the token map is of another batch or device");
+            lead = {T};
+            seq = tokens.attr("seq").cast<Tensor>();
+            pos = tokens.attr("pos").cast<Tensor>();
+            slot = tokens.attr("slot").cast<Tensor>();
+            after = tokens.attr("len_after").cast<Tensor>();
+            TORCH_CHECK_VALUE(seq.device() == dev, "the token map is of another batch or device");
+            need(seq, "seq", at::kInt, {T}, dev);
+            need(pos, "pos", at::kInt, {T}, dev);
+            if (slot.numel() != 0) need(slot, "slot", at::kLong, {T}, dev);   // none: read through the page table
+            need(after, "len_after", at::kInt, {B}, dev);
+            map.seq = ints(seq);
+            map.pos = ints(pos);
+            map.slot = slot.numel() ? static_cast<const int64_t*>(slot.data_ptr()) : nullptr;
+            map.len_after = ints(after);
+        } else {
+            TORCH_CHECK_VALUE(k.dim() == 4 && k.size(0) == B, "a padded batch is [", B, "][tokens][heads][", d, "]");
+            lead = {k.size(0), k.size(1)};
+            if (n_new) need(*n_new, "n_new", at::kInt, {B}, dev);
+        }
+        need(len_before, "len_before", at::kInt, {B}, dev);
+        const duo_rows kr = rows_of(k, "k", n_kv, d, lead, dev), vr = rows_of(v, "v", n_kv, d, lead, dev);
+        const c10::cuda::CUDAGuard guard(dev);
+        duo_rows qr{};
+        OptTensor out;
+        if (q) {
+            qr = rows_of(*q, "q", hq, d, lead, dev);
+            std::vector<int64_t> shape = lead;
+            shape.push_back(hq);
+            shape.push_back(d);
+            if (given) {
+                need(*given, "out", at::kBFloat16, shape, dev);
+                out = given;
+            } else {        // rows without a token are zero where out is new
+                out = ragged || n_new ? at::zeros(shape, k.options()) : at::empty(shape, k.options());
+            }
+        } else {
+            TORCH_CHECK_VALUE(!given, "out without q");
+        }
+        TORCH_CHECK_VALUE(lead.back() <= std::numeric_limits<int32_t>::max(), "too many tokens");
+        check(duo_kv_append_rope(kv, int32_t(layer), reinterpret_cast<const duo_rope*>(rope), q ? &qr : nullptr, &kr, &vr,
+                                 ints(len_before), ragged ? &map : nullptr, ints(n_new), int32_t(lead.back()),
+                                 out ? static_cast<uint16_t*>(out->data_ptr()) : nullptr, stream_of(dev)),
+              "duo_kv_append_rope");
+        return out;
+    }
+
+    py::object reserve(const Tensor& len_before, const OptTensor& n_new, const py::object& tokens) const {
+        need(len_before, "len_before", at::kInt, {B}, dev);
+        if (n_new) need(*n_new, "n_new", at::kInt, {B}, dev);
+        const c10::cuda::CUDAGuard guard(dev);
+        if (tokens.is_none()) {
+            Tensor after = at::empty({B}, len_before.options());
+            check(duo_kv_reserve(kv, ints(len_before), ints(n_new), 0, static_cast<int32_t*>(after.data_ptr()), nullptr,
+                                 nullptr, nullptr, nullptr, stream_of(dev)),
+                  "duo_kv_reserve");
+            return py::cast(after);
+        }
+        const int64_t T = tokens.attr("max_tokens").cast<int64_t>();
+        TORCH_CHECK_VALUE(tokens.attr("batch").cast<int64_t>() == B, "the token map is of another batch or device");
+        const Tensor seq = tokens.attr("seq").cast<Tensor>(), pos = tokens.attr("pos").cast<Tensor>(),
+                     slot = tokens.attr("slot").cast<Tensor>(), after = tokens.attr("len_after").cast<Tensor>(),
+                     cu = tokens.attr("cu").cast<Tensor>();
+        TORCH_CHECK_VALUE(seq.device() == dev, "the token map is of another batch or device");
+        need(seq, "seq", at::kInt, {T}, dev);
+        need(pos, "pos", at::kInt, {T}, dev);
+        need(slot, "slot", at::kLong, {T}, dev);
+        need(after, "len_after", at::kInt, {B}, dev);
+        need(cu, "cu", at::kInt, {B + 1}, dev);
+        TORCH_CHECK_VALUE(T <= std::numeric_limits<int32_t>::max(), "too many tokens");
+        // a map without entries still has its counts: the arrays are not looked at
+        void* const none = cu.data_ptr();
+        check(duo_kv_reserve(kv, ints(len_before), ints(n_new), int32_t(T), static_cast<int32_t*>(after.data_ptr()),
+                             static_cast<int32_t*>(cu.data_ptr()), static_cast<int32_t*>(T ? seq.data_ptr() : none),
+                             static_cast<int32_t*>(T ? pos.data_ptr() : none),
+                             static_cast<int64_t*>(T ? slot.data_ptr() : none), stream_of(dev)),
+              "duo_kv_reserve");
+        return tokens;
+    }
+
+    // out, lse and q_rot come checked or new
+    py::object step_rope(int64_t layer, uintptr_t rope, int64_t rope_d, const Tensor& q, const Tensor& k, const Tensor& v,
+                         const Tensor& len_before, const Tensor& lengths, double scale, const OptTensor& given_out,
+                         const OptTensor& given_lse, bool want_lse, const OptTensor& given_rot, const Tensor& ws) const {
+        TORCH_CHECK_VALUE(rope_d == d, "rope of head_dim ", rope_d, ", expected ", d);
+        const duo_rows qr = rows_of(q, "q", hq, d, {B}, dev), kr = rows_of(k, "k", n_kv, d, {B}, dev),
+                       vr = rows_of(v, "v", n_kv, d, {B}, dev);
+        need(len_before, "len_before", at::kInt, {B}, dev);
+        need(lengths, "lengths", at::kInt, {B}, dev);
+        const c10::cuda::CUDAGuard guard(dev);
+        if (given_rot) need(*given_rot, "q_rot", at::kBFloat16, {B, hq, d}, dev);
+        if (given_out) need(*given_out, "out", at::kFloat, {B, hq, d}, dev);
+        if (given_lse) need(*given_lse, "lse", at::kFloat, {B, hq}, dev);
+        const auto fp32 = q.options().dtype(at::kFloat);
+        const Tensor rot = given_rot ? *given_rot : at::empty({B, hq, d}, q.options());
+        const Tensor out = given_out ? *given_out : at::empty({B, hq, d}, fp32);
+        OptTensor lse = given_lse;
+        if (want_lse && !lse) lse = at::empty({B, hq}, fp32);
+        check(duo_decode_step_rope(kv, int32_t(layer), reinterpret_cast<const duo_rope*>(rope), &qr, &kr, &vr,
+                                   ints(len_before), ints(lengths), float(scale), static_cast<uint16_t*>(rot.data_ptr()),
+                                   static_cast<float*>(out.data_ptr()),
+                                   lse ? static_cast<float*>(lse->data_ptr()) : nullptr, ws.data_ptr(), ws.numel(),
+                                   stream_of(dev)),
+              "duo_decode_step_rope");
+        if (lse) return py::make_tuple(out, *lse);
+        return py::cast(out);
+    }
+};
+
+// ------------------------------------------------------------------ windowed attention
+// One status word per device, never freed: kernels may still hold it when the process ends.
+Tensor status_word(const at::Device& dev) {
+    static std::mutex lock;
+    static auto* words = new std::vector<Tensor>();
+    const std::lock_guard<std::mutex> hold(lock);
+    const size_t i = size_t(dev.index());
+    if (words->size() <= i) words->resize(i + 1);
+    if (!(*words)[i].defined()) {
+        const c10::cuda::CUDAGuard guard(dev);
+        (*words)[i] = at::zeros({1}, at::TensorOptions().dtype(at::kInt).device(dev));
+    }
+    return (*words)[i];
+}
+
+// x, or a copy that the kernels can read: contiguous heads, strides in 16-byte steps and none of them 0.
+Tensor usable(const Tensor& x) {
+    bool ok = x.stride(3) == 1 && reinterpret_cast<uintptr_t>(x.data_ptr()) % 16 == 0;
+    for (int i = 0; ok && i < 3; ++i)
+        if (x.size(i) > 1) ok = x.stride(i) % 8 == 0 && x.stride(i) >= x.size(3);
+    return ok ? x : x.clone(at::MemoryFormat::Contiguous);
+}
+
+// A new dense tensor with x's shape and order of dimensions.
+Tensor like(const Tensor& x) {
+    int order[3] = {0, 1, 2};
+    if (x.numel() > 0)
+        std::stable_sort(order, order + 3, [&](int a, int b) { return x.stride(a) > x.stride(b); });
+    int64_t strides[4] = {0, 0, 0, 1}, step = x.size(3);
+    for (int i = 2; i >= 0; --i) {
+        strides[order[i]] = step;
+        step *= std::max<int64_t>(x.size(order[i]), 1);
+    }
+    return at::empty_strided(x.sizes(), strides, x.options());
+}
+
+duo_heads heads_of(const Tensor& x) { return duo_heads{x.data_ptr(), x.stride(0), x.stride(1), x.stride(2)}; }
+
+struct Shape {
+    int64_t sink, window;
+    double scale;
+};
+
+duo_window_attn_desc desc_of(const Tensor& q, const Tensor& k, const Shape& s, const Tensor& lengths) {
+    duo_window_attn_desc d{};
+    d.dtype = rope_dtype(q.scalar_type());
+    d.batch = int32_t(q.size(0));
+    d.num_q_heads = int32_t(q.size(1));
+    d.num_kv_heads = int32_t(k.size(1));
+    d.head_dim = int32_t(q.size(3));
+    d.tokens = int32_t(q.size(2));
+    d.sink = int32_t(s.sink);
+    d.window = int32_t(s.window);
+    d.scale = float(s.scale);
+    d.lengths = lengths.defined() ? ints(lengths) : nullptr;
+    return d;
+}
+
+struct WindowAttention : torch::autograd::Function<WindowAttention> {
+    static Tensor forward(torch::autograd::AutogradContext* ctx, const Tensor& q0, const Tensor& k0, const Tensor& v0,
+                          const OptTensor& given, int64_t sink, int64_t window, double scale) {
+        const Tensor lengths = given ? *given : Tensor();
+        const c10::cuda::CUDAGuard guard(q0.device());
+        const Tensor q = usable(q0), k = usable(k0), v = usable(v0);
+        const duo_window_attn_desc d = desc_of(q, k, {sink, window, scale}, lengths);
+        size_t bytes = 0;
+        check(duo_window_attn_stats_bytes(&d, &bytes), "duo_window_attn");
+        const Tensor out = like(q);
+        const Tensor stats = at::empty({int64_t(bytes)}, q.options().dtype(at::kByte));
+        const duo_heads hq = heads_of(q), hk = heads_of(k), hv = heads_of(v), ho = heads_of(out);
+        check(duo_window_attn(&d, &hq, &hk, &hv, &ho, static_cast<float*>(stats.data_ptr()),
+                              static_cast<int32_t*>(status_word(q.device()).data_ptr()), stream_of(q.device())),
+              "duo_window_attn");
+        ctx->save_for_backward({q, k, v, out, stats, lengths});
+        ctx->saved_data["sink"] = sink;
+        ctx->saved_data["window"] = window;
+        ctx->saved_data["scale"] = scale;
+        return out;
+    }
+
+    static torch::autograd::variable_list backward(torch::autograd::AutogradContext* ctx,
+                                                   torch::autograd::variable_list grads) {
+        const auto saved = ctx->get_saved_variables();
+        const Tensor &q = saved[0], &k = saved[1], &v = saved[2], &out = saved[3], &stats = saved[4], &lengths = saved[5];
+        const c10::cuda::CUDAGuard guard(q.device());
+        torch::autograd::variable_list res(7);
+        {
+            const at::AutoGradMode off(false);
+            const Tensor g = usable(grads[0]);
+            const Shape s{ctx->saved_data["sink"].toInt(), ctx->saved_data["window"].toInt(),
+                          ctx->saved_data["scale"].toDouble()};
+            const duo_window_attn_desc d = desc_of(q, k, s, lengths);
+            size_t bytes = 0;
+            check(duo_window_attn_workspace_bytes(&d, &bytes), "duo_window_attn_grad");
+            const Tensor dq = like(q), dk = like(k), dv = like(v);
+            const Tensor ws = at::empty({int64_t(std::max<size_t>(bytes, 256))}, q.options().dtype(at::kByte));
+            const duo_heads h[8] = {heads_of(q), heads_of(k),  heads_of(v),  heads_of(out),
+                                    heads_of(g), heads_of(dq), heads_of(dk), heads_of(dv)};
+            check(duo_window_attn_grad(&d, &h[0], &h[1], &h[2], &h[3], &h[4], static_cast<const float*>(stats.data_ptr()),
+                                       &h[5], &h[6], &h[7], ws.data_ptr(), ws.numel(),
+                                       static_cast<int32_t*>(status_word(q.device()).data_ptr()), stream_of(q.device())),
+                  "duo_window_attn_grad");
+            const Tensor* got[3] = {&dq, &dk, &dv};
+            for (int i = 0; i < 3; ++i)
+                if (ctx->needs_input_grad(i)) res[i] = *got[i];
+        }
+        if (at::GradMode::is_enabled()) {       // create_graph: the gradients exist, theirs do not
+            torch::autograd::variable_list some;
+            for (int i = 0; i < 3; ++i)
+                if (res[i].defined()) some.push_back(res[i].set_requires_grad(true));
+            const auto err = std::make_shared<torch::autograd::DelayedError>(
+                "window_attention is differentiable once: its gradients have none", int64_t(some.size()));
+            const auto marked = (*err)(std::move(some));
+            for (int i = 0, j = 0; i < 3; ++i)
+                if (res[i].defined()) res[i] = marked[j++];
+        }
+        return res;
+    }
+};
+
+Tensor window_attention(const Tensor& q, const Tensor& k, const Tensor& v, int64_t sink, std::optional<int64_t> window,
+                        const OptTensor& lengths, std::optional<double> given_scale) {
+    const Tensor* in[3] = {&q, &k, &v};
+    const char* names[3] = {"q", "k", "v"};
+    for (int i = 0; i < 3; ++i) {
+        const Tensor& t = *in[i];
+        TORCH_CHECK_TYPE((t.scalar_type() == at::kBFloat16 || t.scalar_type() == at::kHalf) &&
+                             t.scalar_type() == q.scalar_type(),
+                         names[i], ": dtype ", t.scalar_type(), ", expected bfloat16 or float16, the same for q, k and v");
+        TORCH_CHECK_VALUE(t.is_cuda() && t.device() == q.device(), names[i], ": on ", t.device(),
+                          ", expected one CUDA device for q, k and v");
+        TORCH_CHECK_VALUE(t.dim() == 4, names[i], ": shape ", shape_of(t.sizes()), ", expected [batch][heads][tokens][128]");
+    }
+    const int64_t B = q.size(0), hq = q.size(1), T = q.size(2), d = q.size(3), n_kv = k.size(1);
+    TORCH_CHECK_VALUE(k.sizes() == v.sizes() && k.size(0) == B && k.size(2) == T && k.size(3) == d, "k, v: shapes ",
+                      shape_of(k.sizes()), ", ", shape_of(v.sizes()), ", expected (", B, ", key heads, ", T, ", ", d, ")");
+    TORCH_CHECK_VALUE(d == 128, "heads of ", d, " elements, expected 128");
+    TORCH_CHECK_VALUE(n_kv >= 1 && hq >= 1 && hq % n_kv == 0, hq, " query heads over ", n_kv, " key heads");
+    TORCH_CHECK_VALUE(sink >= 0 && (!window || *window >= 1), "sink must be at least 0 and window at least 1 (or None)");
+    if (lengths)
+        TORCH_CHECK_VALUE(lengths->scalar_type() == at::kInt && lengths->device() == q.device() &&
+                              lengths->sizes() == at::IntArrayRef({B}) && lengths->is_contiguous(),
+                          "lengths must be contiguous int32 [", B, "] on the tensors' device");
+    const double scale = given_scale ? *given_scale : 0.08838834764831845;      // 128 ** -0.5
+    TORCH_CHECK_VALUE(scale > 0 && scale < 1e30, "scale must be above 0");
+    const int64_t top = std::numeric_limits<int32_t>::max();
+    TORCH_CHECK_VALUE(B <= top && T <= top && hq <= top, "too large a tensor");
+    return WindowAttention::apply(q, k, v, lengths, std::min(sink, top),
+                                  window ? std::min(*window, top) : int64_t(0), scale);
+}
+
+int64_t window_attention_status(int64_t device, bool clear) {
+    const at::Device dev(at::kCUDA, at::DeviceIndex(device));
+    const c10::cuda::CUDAGuard guard(dev);
+    Tensor word = status_word(dev);
+    const int64_t bits = word.item<int32_t>();
+    if (clear) word.zero_();
+    return bits;
+}
+
+}  // namespace
+
+PYBIND11_MODULE(TORCH_EXTENSION_NAME, m) {
+    py::register_exception_translator([](std::exception_ptr e) {
+        try {
+            if (e) std::rethrow_exception(e);
+        } catch (const DuoFailure& f) {
+            const py::object type = py::module_::import("head_wise_kv_b200._lib").attr("DuoError");
+            PyErr_SetObject(type.ptr(), type(f.code, f.what_call).ptr());
+        }
+    });
+    m.def("rope_apply", &rope_apply);
+    py::class_<Cache>(m, "Cache")
+        .def(py::init<uintptr_t, int64_t, int64_t, int64_t, int64_t, int64_t>())
+        .def("append_rope", &Cache::append_rope)
+        .def("reserve", &Cache::reserve)
+        .def("step_rope", &Cache::step_rope);
+    m.def("window_attention", &window_attention);
+    m.def("window_attention_status", &window_attention_status);
+}

@@ -5,6 +5,7 @@ from __future__ import annotations
 import torch
 
 from . import _lib as L
+from . import _binding as _b
 
 _DTYPE = {torch.bfloat16: L.DUO_BF16, torch.float16: L.DUO_FP16, torch.float32: L.DUO_FP32}
 _LAYOUT = {"half": L.DUO_ROPE_HALF, "interleaved": L.DUO_ROPE_INTERLEAVED}
@@ -113,11 +114,7 @@ class Rope:
         return self._apply(x, positions, n_new, transpose, out)
 
     def _apply(self, x, positions, n_new, transpose, out):
-        if out is None:
-            make = torch.empty if n_new is None else torch.zeros
-            out = make(x.shape, dtype=x.dtype, device=x.device)
-        self.launch([(x, out, True)], positions, n_new, transpose)
-        return out
+        return _b.rope_apply(self.handle or 0, self.d, x, positions, n_new, transpose, out)
 
 
 class _RopeFunction(torch.autograd.Function):
