@@ -311,6 +311,7 @@ int duo_kv_append_rope(duo_kv* kv, int32_t layer, const duo_rope* rope, const du
     p.n_new = n_new;
     p.n = n_tokens;
     p.T = map ? int64_t(n_tokens) : int64_t(n_tokens) * kv->desc.batch;
+    if (p.T > 0x7fffffff) return DUO_ERR_UNSUPPORTED;
     p.kr = reinterpret_cast<uint16_t*>(kv->base + L.off_kr);
     p.vr = reinterpret_cast<uint16_t*>(kv->base + L.off_vr);
     p.ks = reinterpret_cast<uint16_t*>(kv->base + L.off_ks);

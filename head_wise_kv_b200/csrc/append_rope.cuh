@@ -31,7 +31,8 @@ struct AppendRopeParams {
     int64_t num_pages;
     int max_pages;
     const int32_t* page_table;
-    int heads_per_thread;
+    int per_thread;               // heads per thread
+    int groups;                   // of heads, each a block per 8 tokens
     RopeTable table;
     int32_t rank[kMaxKvHeads];
     uint8_t is_r[kMaxKvHeads];

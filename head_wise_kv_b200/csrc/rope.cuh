@@ -60,22 +60,25 @@ __device__ __forceinline__ RopeUnit rope_unit(const RopeTable& t, int u) {
     return r;
 }
 
-// Cosine and sine, times the magnitude, of pairs 8u .. 8u + 7 at position p.
-// The nearest quarter turn is taken off in fixed point, so that what becomes
-// fp32 is at most 1/8 of a turn: its rounding moves the angle by at most
-// 2^-25 of itself, below the rounding of the sine.
+// Cosine and sine, times the magnitude, of a pair at position p.  The nearest
+// quarter turn is taken off in fixed point, so that what becomes fp32 is at
+// most 1/8 of a turn: its rounding moves the angle by at most 2^-25 of itself,
+// below the rounding of the sine.
+__device__ __forceinline__ void rope_angle(const RopeTable& t, int pair, int p, float sign, float& c, float& s) {
+    const uint64_t a = uint64_t(int64_t(p)) * t.turn[pair];
+    const uint32_t quarter = uint32_t((a + (uint64_t(1) << 61)) >> 62);
+    const int64_t rest = int64_t(a - (uint64_t(quarter) << 62));
+    float sn, cs;
+    sincospif(float(rest) * 1.0842021724855044e-19f, &sn, &cs);      // 2^-63: in half turns
+    const float cq = quarter & 1 ? sn : cs, sq = quarter & 1 ? cs : sn;
+    c = (((quarter + 1) & 2) ? -cq : cq) * t.magnitude;
+    s = ((quarter & 2) ? -sq : sq) * t.magnitude * sign;
+}
+
+// The same of pairs 8u .. 8u + 7.
 __device__ __forceinline__ void rope_angles(const RopeTable& t, int u, int p, float sign, float (&c)[8], float (&s)[8]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint64_t a = uint64_t(int64_t(p)) * t.turn[8 * u + i];
-        const uint32_t quarter = uint32_t((a + (uint64_t(1) << 61)) >> 62);
-        const int64_t rest = int64_t(a - (uint64_t(quarter) << 62));
-        float sn, cs;
-        sincospif(float(rest) * 1.0842021724855044e-19f, &sn, &cs);      // 2^-63: in half turns
-        const float cq = quarter & 1 ? sn : cs, sq = quarter & 1 ? cs : sn;
-        c[i] = (((quarter + 1) & 2) ? -cq : cq) * t.magnitude;
-        s[i] = ((quarter & 2) ? -sq : sq) * t.magnitude * sign;
-    }
+    for (int i = 0; i < 8; ++i) rope_angle(t, 8 * u + i, p, sign, c[i], s[i]);
 }
 
 // x[0..7] and x[8..15] are the unit's two vectors.
