@@ -16,7 +16,8 @@
 // visible pair are visited.
 //
 // Precision: products take bf16 (fp16) operands and sum in fp32; scores,
-// softmax statistics, sums and D are fp32.  p_ij and ds_ij are rounded to the
+// softmax statistics, sums and D are fp32
+// (D from the result before its rounding, as far as 8 more bits hold it).  p_ij and ds_ij are rounded to the
 // inputs' type because a tcgen05 product needs both operands in one 16-bit
 // type: relative 2^-9 per element, averaged over the sums, the size of the
 // rounding of the result.
@@ -94,27 +95,37 @@ __device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
 }
 
 // Bounded waits of one CTA: the first that runs out marks the CTA, and every
-// role leaves at its next wait.
+// role leaves at its next wait.  A warp waits with all its lanes: a wait by
+// one lane and the reconvergence behind it take about 500 cycles even where
+// the phase has completed, one by all lanes about 120 (backward of 4096
+// tokens x 32 heads: 587 us with the former in every role).
 struct Waiter {
     int32_t* status;
     unsigned long long limit;
     volatile int* abort_flag;
 
-    __device__ __forceinline__ bool timed(uint32_t bar, uint32_t parity) const {
-        if (*abort_flag) return false;
-        if (mbar_wait(bar, parity, limit)) return true;
+    __device__ __forceinline__ bool gave_up(unsigned long long t0) const {
+        if (*abort_flag) return true;
+        if (global_ns() - t0 <= limit) return false;
         if (status) set_status(status, DUO_STATUS_WAIT_TIMEOUT);
         *abort_flag = 1;
-        return false;
+        return true;
     }
-    // the whole warp: lane 0 waits for it
+    // one thread, alone in its warp's path
+    __device__ __forceinline__ bool thread(uint32_t bar, uint32_t parity) const {
+        if (mbar_try_wait(bar, parity)) return true;
+        const unsigned long long t0 = global_ns();
+        while (!mbar_try_wait(bar, parity))
+            if (gave_up(t0)) return false;
+        return true;
+    }
+    // a converged warp
     __device__ __forceinline__ bool warp(uint32_t bar, uint32_t parity) const {
-        if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
-        int ok = 1;
-        if ((threadIdx.x & 31) == 0) ok = timed(bar, parity) ? 1 : 0;
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        __syncwarp();
-        return ok != 0;
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+        const unsigned long long t0 = global_ns();
+        while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity)))
+            if (__any_sync(0xffffffffu, gave_up(t0))) return false;
+        return true;
     }
 };
 
@@ -142,16 +153,15 @@ __device__ __forceinline__ void bulk_row(uint32_t dst, const float* src, uint32_
         : "memory");
 }
 
-// Rows [first, 128) of a tile become zeros (one warp): a product must not
-// meet what lies behind a sequence's last token, since 0 x NaN is NaN.
-__device__ __forceinline__ void zero_rows(uint32_t tile, int first) {
-    const int lane = threadIdx.x & 31;
-    for (int off = first * 128 + lane * 16; off < int(kSlab); off += 32 * 16) {
+// Rows [first, 128) of a tile become zeros, by `warps` warps of which this is
+// number w: a product must not meet what lies behind a sequence's last token,
+// since 0 x NaN is NaN.  The products must wait for these warps.
+__device__ __forceinline__ void zero_rows(uint32_t tile, int first, int w, int warps) {
+    for (int off = first * 128 + (w * 32 + int(threadIdx.x & 31)) * 16; off < int(kSlab); off += warps * 32 * 16) {
         st_shared_v4(tile + off, make_uint4(0, 0, 0, 0));
         st_shared_v4(tile + kSlab + off, make_uint4(0, 0, 0, 0));
     }
     fence_proxy_async_smem();
-    __syncwarp();
 }
 
 // D (+)= A B^T: both tiles with their 128 dims along K.
@@ -214,127 +224,216 @@ __device__ __forceinline__ T* row_at(const HeadTensor& x, int b, int h, int t) {
     return static_cast<T*>(x.data) + b * x.b + h * x.h + t * x.t;
 }
 
+// ------------------------------------------------------------------ shared memory
+// Both kernels use seven tiles and a little more, of the 227 KB that a CTA
+// may have.  The dynamic region starts at a multiple of 1024 bytes (there is
+// no static one before it); the kernels leave with a status bit if not.
+constexpr int kThreads = 320;                        // warps 0-7 elementwise, 8 TMA, 9 products
+constexpr uint32_t kStatsAt = 7 * kTileBytes;        // [3][128] row statistics, [2][128] minus D
+constexpr uint32_t kBarsAt = kStatsAt + 5 * kTile * 4;
+constexpr int kRing3 = 3, kRing2 = 2;                // stages of the two rings of tiles
+
+struct Bars {
+    uint64_t once, full3[kRing3], empty3[kRing3], full2[kRing2], empty2[kRing2];
+    uint64_t s_full[2], s_read, dp_full, dp_read, p_full[2], ds_full, trimmed, done[2];
+    uint32_t tmem;
+    int abort_flag;
+};
+constexpr uint32_t kSmem = kBarsAt + sizeof(Bars);
+static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
+
+__device__ __forceinline__ Bars& bars_of(unsigned char* raw) { return *reinterpret_cast<Bars*>(raw + kBarsAt); }
+
+// Barriers (one arrival each unless said) and TMEM, by every warp of the CTA.
+__device__ __forceinline__ void set_up(Bars& sh, int p_arrivals) {
+    if (threadIdx.x == 0) {
+        for (uint64_t* bar = &sh.once; bar < reinterpret_cast<uint64_t*>(&sh.tmem); ++bar) mbar_init(smem_addr(bar), 1);
+        for (uint64_t* bar : {&sh.s_read, &sh.dp_read, &sh.ds_full, &sh.trimmed}) mbar_init(smem_addr(bar), 8);
+        for (uint64_t* bar : {&sh.p_full[0], &sh.p_full[1]}) mbar_init(smem_addr(bar), p_arrivals);
+        sh.abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (threadIdx.x >> 5 == 9) tmem_alloc(smem_addr(&sh.tmem), 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+}
+
+__device__ __forceinline__ void tear_down(Bars& sh) {
+    tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x >> 5 == 9) {
+        tc_fence_after();
+        tmem_dealloc(sh.tmem, 512);
+    }
+}
+
+// The last copies of a ring have landed (a CTA must not leave before).
+template <int STAGES>
+__device__ __forceinline__ void drain(uint64_t* full, int issued, unsigned long long limit) {
+    for (int k = 1; k <= STAGES && k <= issued; ++k)
+        mbar_wait(smem_addr(&full[(issued - k) % STAGES]), ((issued - k) / STAGES) & 1, limit);
+}
+
+// This thread's warp has reached a point: one arrival, predicated (a branch
+// for one lane would cost its reconvergence).
+__device__ __forceinline__ void arrive_warp(uint64_t* bar) {
+    tc_fence_before();
+    __syncwarp();
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.eq.u32 p, %1, 0;\n\t"
+        "@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(smem_addr(bar)),
+        "r"(threadIdx.x & 31)
+        : "memory");
+}
+
 // ------------------------------------------------------------------ forward
-// One CTA per (sequence, query head, query tile), 6 warps; two CTAs share an
-// SM, so that one's products run under the other's softmax, and one's
-// start and end under the other's middle.
-//   warp 0: TMA (Q once, K and V tiles one ahead)
-//   warp 1: products: S_j = Q K_j^T, O += P_j V_j (P_j from TMEM)
-//   warps 2-5: softmax, a thread per row: running maximum with lazy
-//     rescaling (O is rescaled only where the maximum grows by more than
-//     2^8), P_j over S_j in TMEM, O / l at the end.
-constexpr int kFwdThreads = 192;
-constexpr uint32_t kFwdSmem = 3 * kTileBytes + 1024;
-constexpr uint32_t kFwdCols = 256, kFwdS = 0, kFwdO = 128;
+// One CTA per (sequence, query head, two query tiles a and b), which share
+// the key tiles that pass: Q stays, K in a ring of three tiles, V of two (a
+// load takes about 2500 cycles under load, so each is asked for a whole tile
+// pair ahead).
+//   products: S = Q K_j^T, O += P_j V_j, P_j over S in TMEM as the A operand:
+//     PV_a(j), S_a(j+1), PV_b(j), S_b(j+1), so that one tile's products run
+//     under the other's softmax
+//   warps 0-3, 4-7: softmax of a and b, a thread per row: running maximum
+//     with lazy rescaling (O is rescaled only where the maximum grows by more
+//     than 2^8), P_j, O / l at the end.
+// Beside the result each row leaves its statistics and what the rounding of
+// the result took away (in 8 bits), for D_i in the backward.
+constexpr float kLowScale = 1024.f;      // of the rounding's remainder: 2^-26 .. 56 without loss of its leading bits
+
+// The key tiles of two neighbouring query tiles: those of the first and of
+// the second one in one list.
+struct PairTiles {
+    int qa, lo_b, sink_tiles, sinks, lo, hi, n;
+    bool full;
+    __device__ __forceinline__ PairTiles(const WindowAttnParams& p, int pair, int len) {
+        qa = 2 * pair;
+        full = p.full;
+        hi = (qa + 1) * kTile < len ? qa + 1 : qa;
+        sink_tiles = p.full ? 0 : (p.S + kTile - 1) / kTile;
+        lo = p.full ? 0 : max(0, qa * kTile - p.W + 1) / kTile;
+        lo_b = p.full ? 0 : max(0, (qa + 1) * kTile - p.W + 1) / kTile;
+        sinks = min(sink_tiles, lo);
+        n = sinks + hi - lo + 1;
+    }
+    __device__ __forceinline__ int at(int j) const { return j < sinks ? j : lo + j - sinks; }
+    // whether query tile qa + x visits key tile kt of the list
+    __device__ __forceinline__ bool visits(int x, int kt) const {
+        return x == 0 ? kt <= qa : hi > qa && (kt >= lo_b || kt < sink_tiles);
+    }
+    __device__ __forceinline__ bool last(int x, int kt) const { return kt == qa + x; }
+};
 
 template <typename T>
-__global__ void __launch_bounds__(kFwdThreads, 2) window_fwd_kernel(const __grid_constant__ WindowAttnParams p) {
-    extern __shared__ unsigned char smem_raw[];
-    __shared__ __align__(8) uint64_t q_full, k_full, k_empty, v_full, v_empty, s_full, p_full, done;
-    __shared__ uint32_t tmem_sh;
-    __shared__ int abort_sh;
+__global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_constant__ WindowAttnParams p) {
+    extern __shared__ __align__(1024) unsigned char raw[];
     constexpr uint32_t kQK = idesc_f16(kTile, kTile, Elem<T>::bf16, false, false);
     constexpr uint32_t kPV = idesc_f16(kTile, kTile, Elem<T>::bf16, false, true);
-    const uint32_t sQ = (smem_addr(smem_raw) + 1023) & ~1023u, sK = sQ + kTileBytes, sV = sK + kTileBytes;
+    Bars& sh = bars_of(raw);
+    const uint32_t smem = smem_addr(raw), sQ = smem, sK = sQ + 2 * kTileBytes, sV = sK + kRing3 * kTileBytes;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-
+    if (smem & 1023u) {
+        if (p.status && threadIdx.x == 0) set_status(p.status, DUO_STATUS_WAIT_TIMEOUT);
+        return;
+    }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     // the query tiles with most keys first
     const int heads = p.B * p.hq;
-    const int qt = p.n_t - 1 - int(blockIdx.x) / heads;
+    const int pair = (p.n_t + 1) / 2 - 1 - int(blockIdx.x) / heads;
     const int b = int(blockIdx.x) % heads / p.hq, h = int(blockIdx.x) % p.hq, g = h / p.G;
-    const int len = length_of(p, b), i0 = qt * kTile;
+    const int len = length_of(p, b), i0 = 2 * pair * kTile;
+    const int64_t row0 = (int64_t(b) * p.hq + h) * p.Tp;
     if (i0 >= len) {        // no row of a sequence: zeros
-        for (int x = threadIdx.x; x < kTile * 16; x += kFwdThreads) {
+        for (int x = threadIdx.x; x < 2 * kTile * 16; x += kThreads) {
             const int t = i0 + x / 16;
             if (t < p.T) *reinterpret_cast<uint4*>(row_at<T>(p.out, b, h, t) + x % 16 * 8) = make_uint4(0, 0, 0, 0);
         }
-        if (threadIdx.x < kTile) p.stats[(int64_t(b) * p.hq + h) * p.Tp + i0 + threadIdx.x] = -CUDART_INF_F;
+        for (int t = i0 + threadIdx.x; t < min(i0 + 2 * kTile, p.Tp); t += kThreads) p.stats[row0 + t] = -CUDART_INF_F;
         return;
     }
-    const KeyTiles tiles(p, qt);
-    const bool cut = i0 + kTile > len && len < p.T;     // the last key tile reaches behind the sequence
+    const PairTiles tiles(p, pair, len);
+    set_up(sh, 4);
+    const uint32_t tmem = sh.tmem;
+    const Waiter wait{p.status, p.timeout_ns, &sh.abort_flag};
 
-    if (threadIdx.x == 0) {
-        for (uint64_t* bar : {&q_full, &k_full, &k_empty, &v_full, &v_empty, &s_full, &done})
-            mbar_init(smem_addr(bar), 1);
-        mbar_init(smem_addr(&p_full), 4);
-        abort_sh = 0;
-        fence_mbar_init();
-    }
-    if (warp == 1) tmem_alloc(smem_addr(&tmem_sh), kFwdCols);
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = tmem_sh;
-    const Waiter wait{p.status, p.timeout_ns, &abort_sh};
-
-    if (warp == 0) {
+    if (warp == 8) {
         if (lane == 0) {
-            mbar_arrive_expect_tx(smem_addr(&q_full), kTileBytes);
-            tma_tile(sQ, &p.tm_q, i0, h, b, smem_addr(&q_full));
+            const bool two = tiles.hi > tiles.qa;
+            mbar_arrive_expect_tx(smem_addr(&sh.once), (two ? 2 : 1) * kTileBytes);
+            tma_tile(sQ, &p.tm_q, i0, h, b, smem_addr(&sh.once));
+            if (two) tma_tile(sQ + kTileBytes, &p.tm_q, i0 + kTile, h, b, smem_addr(&sh.once));
             int ks = 0, vs = 0;
             for (int j = 0; j < tiles.n; ++j) {
                 const int t = tiles.at(j) * kTile;
-                if (!wait.timed(smem_addr(&k_empty), (j & 1) ^ 1)) break;
-                mbar_arrive_expect_tx(smem_addr(&k_full), kTileBytes);
-                tma_tile(sK, &p.tm_k, t, g, b, smem_addr(&k_full));
+                if (!wait.thread(smem_addr(&sh.empty3[j % kRing3]), ((j / kRing3) & 1) ^ 1)) break;
+                mbar_arrive_expect_tx(smem_addr(&sh.full3[j % kRing3]), kTileBytes);
+                tma_tile(sK + j % kRing3 * kTileBytes, &p.tm_k, t, g, b, smem_addr(&sh.full3[j % kRing3]));
                 ++ks;
-                if (!wait.timed(smem_addr(&v_empty), (j & 1) ^ 1)) break;
-                mbar_arrive_expect_tx(smem_addr(&v_full), kTileBytes);
-                tma_tile(sV, &p.tm_v, t, g, b, smem_addr(&v_full));
+                if (!wait.thread(smem_addr(&sh.empty2[j % kRing2]), ((j / kRing2) & 1) ^ 1)) break;
+                mbar_arrive_expect_tx(smem_addr(&sh.full2[j % kRing2]), kTileBytes);
+                tma_tile(sV + j % kRing2 * kTileBytes, &p.tm_v, t, g, b, smem_addr(&sh.full2[j % kRing2]));
                 ++vs;
             }
-            // no copy may land after this CTA has left
-            mbar_wait(smem_addr(&q_full), 0, p.timeout_ns);
-            if (ks > 0) mbar_wait(smem_addr(&k_full), (ks - 1) & 1, p.timeout_ns);
-            if (vs > 0) mbar_wait(smem_addr(&v_full), (vs - 1) & 1, p.timeout_ns);
+            mbar_wait(smem_addr(&sh.once), 0, p.timeout_ns);
+            drain<kRing3>(sh.full3, ks, p.timeout_ns);
+            drain<kRing2>(sh.full2, vs, p.timeout_ns);
         }
-    } else if (warp == 1) {
-        bool ok = wait.warp(smem_addr(&q_full), 0);
-        for (int j = 0; ok && j < tiles.n; ++j) {
-            // S_j takes the place of P_{j-1}: the products run in the order of issue
-            ok = wait.warp(smem_addr(&k_full), j & 1);
-            if (!ok) break;
-            if (lane == 0) {
-                mma_dims(tmem + kFwdS, sQ, sK, kQK);
-                umma_commit(smem_addr(&s_full));
-                umma_commit(smem_addr(&k_empty));
-            }
-            __syncwarp();
-            ok = wait.warp(smem_addr(&v_full), j & 1);
-            if (!ok) break;
-            if (cut && j == tiles.n - 1) zero_rows(sV, len - i0);
-            ok = wait.warp(smem_addr(&p_full), j & 1);
-            if (!ok) break;
-            tc_fence_after();
-            if (lane == 0) {
-                mma_rows(tmem + kFwdO, tmem + kFwdS, 32, sV, kPV, j > 0);
-                umma_commit(smem_addr(&v_empty));
-            }
-            __syncwarp();
-        }
+    } else if (warp == 9) {
         if (lane == 0) {
-            umma_commit(smem_addr(&done));
-            mbar_wait(smem_addr(&done), 0, p.timeout_ns);
+            bool ok = wait.thread(smem_addr(&sh.once), 0);
+            int seen[2] = {0, 0};               // key tiles that a and b have been through
+            // S of both tiles' next key tile and P V of this one, a before b; the
+            // products run in the order of issue, so S may take the place of a P
+            // whose product has been issued
+            for (int j = -1; ok && j < tiles.n; ++j) {
+                const int kt = j < 0 ? -1 : tiles.at(j), next = j + 1 < tiles.n ? tiles.at(j + 1) : -1;
+                const uint32_t k = sK + (j + 1) % kRing3 * kTileBytes, v = sV + max(j, 0) % kRing2 * kTileBytes;
+                if (next >= 0) ok = wait.thread(smem_addr(&sh.full3[(j + 1) % kRing3]), ((j + 1) / kRing3) & 1);
+                if (ok && j >= 0) ok = wait.thread(smem_addr(&sh.full2[j % kRing2]), (j / kRing2) & 1);
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    if (ok && j >= 0 && tiles.visits(x, kt)) {
+                        ok = wait.thread(smem_addr(&sh.p_full[x]), seen[x] & 1);
+                        if (!ok) break;
+                        tc_fence_after();
+                        mma_rows(tmem + 256 + x * 128, tmem + x * 128, 32, v, kPV, seen[x] > 0);
+                        if (tiles.last(x, kt)) umma_commit(smem_addr(&sh.done[x]));
+                        ++seen[x];
+                    }
+                    if (ok && next >= 0 && tiles.visits(x, next)) {
+                        mma_dims(tmem + x * 128, sQ + x * kTileBytes, k, kQK);
+                        umma_commit(smem_addr(&sh.s_full[x]));
+                    }
+                }
+                if (!ok) break;
+                if (next >= 0) umma_commit(smem_addr(&sh.empty3[(j + 1) % kRing3]));
+                if (j >= 0) umma_commit(smem_addr(&sh.empty2[j % kRing2]));
+            }
+            // every product has completed before TMEM is freed
+            umma_commit(smem_addr(&sh.dp_full));
+            mbar_wait(smem_addr(&sh.dp_full), 0, p.timeout_ns);
         }
         __syncwarp();
     } else {
-        const int quarter = warp & 3, r = quarter * 32 + lane, i = i0 + r;
-        const uint32_t at = tmem + (uint32_t(quarter * 32) << 16);
+        const int quarter = warp & 3, x = warp >> 2, qt = tiles.qa + x, r = quarter * 32 + lane, i = qt * kTile + r;
+        const uint32_t at = tmem + (uint32_t(quarter * 32) << 16) + x * 128;
         float m = kNegBig, l = 0.f;
         bool ok = true;
+        int seen = 0;
         for (int j = 0; j < tiles.n; ++j) {
-            ok = wait.warp(smem_addr(&s_full), j & 1);
+            const int kt = tiles.at(j);
+            if (!tiles.visits(x, kt)) continue;
+            ok = wait.warp(smem_addr(&sh.s_full[x]), seen & 1);
             if (!ok) break;
             tc_fence_after();
             float s[128];
             uint32_t* u = reinterpret_cast<uint32_t*>(s);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) tmem_ld32p(at + kFwdS + q * 32, u + q * 32);
+            for (int q = 0; q < 4; ++q) tmem_ld32p(at + q * 32, u + q * 32);
             tmem_wait_ld();
-            const int kt = tiles.at(j);
             if (kt == qt || !whole(p, qt, kt)) {
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
@@ -345,7 +444,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2) window_fwd_kernel(const __grid
             }
             float t8[8];
 #pragma unroll
-            for (int x = 0; x < 8; ++x) t8[x] = s[x];
+            for (int c = 0; c < 8; ++c) t8[c] = s[c];
 #pragma unroll
             for (int c = 8; c < 128; c += 2) t8[(c >> 1) & 7] = fmax3(t8[(c >> 1) & 7], s[c], s[c + 1]);
             const float mx = fmax3(fmax3(t8[0], t8[1], t8[2]), fmax3(t8[3], t8[4], t8[5]), fmaxf(t8[6], t8[7]));
@@ -354,16 +453,16 @@ __global__ void __launch_bounds__(kFwdThreads, 2) window_fwd_kernel(const __grid
             const float m_new = grow ? mt : m;
             const float alpha = fast_exp2(m - m_new);
             m = m_new;
-            // s_full follows O += P_{j-1} V_{j-1} in the order of issue
-            if (j > 0 && __any_sync(0xffffffffu, grow)) {
+            // s_full follows O += P V of the tile before in the order of issue
+            if (seen > 0 && __any_sync(0xffffffffu, grow)) {
 #pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
                     uint32_t o[32];
-                    tmem_ld32(at + kFwdO + c * 32, o);
+                    tmem_ld32(at + 256 + c * 32, o);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * alpha);
-                    tmem_st32(at + kFwdO + c * 32, o);
+                    for (int z = 0; z < 32; ++z) o[z] = __float_as_uint(__uint_as_float(o[z]) * alpha);
+                    tmem_st32(at + 256 + c * 32, o);
                 }
             }
             float2 acc[4] = {};
@@ -373,89 +472,122 @@ __global__ void __launch_bounds__(kFwdThreads, 2) window_fwd_kernel(const __grid
                 uint32_t ph[16];
 #pragma unroll
                 for (int c = 0; c < 32; c += 2) {
-                    const float2 x = ffma2(make_float2(s[q * 32 + c], s[q * 32 + c + 1]), sc2, nm2);
-                    const float2 e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+                    const float2 y = ffma2(make_float2(s[q * 32 + c], s[q * 32 + c + 1]), sc2, nm2);
+                    const float2 e = make_float2(fast_exp2(y.x), fast_exp2(y.y));
                     acc[(c >> 1) & 3] = fadd2(acc[(c >> 1) & 3], e);
                     ph[c / 2] = Elem<T>::pack(e.x, e.y);
                 }
-                tmem_stn<16>(at + kFwdS + q * 16, ph);
+                tmem_stn<16>(at + q * 16, ph);
             }
             const float2 sum = fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3]));
             l = l * alpha + (sum.x + sum.y);
+            if (kt * kTile + kTile > len && len < p.T) {
+                // the sequence ends inside its last key tile (which one query tile visits)
+                ok = wait.warp(smem_addr(&sh.full2[j % kRing2]), (j / kRing2) & 1);
+                if (!ok) break;
+                zero_rows(sV + j % kRing2 * kTileBytes, len - kt * kTile, quarter, 4);
+            }
             tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_addr(&p_full));
+            arrive_warp(&sh.p_full[x]);
+            ++seen;
         }
-        if (ok) ok = wait.warp(smem_addr(&done), 0);
-        if (ok) {
+        if (qt > tiles.hi) {                // the second tile lies behind the sequence
+            if (i < p.T)
+                for (int c = 0; c < kTile; c += 8)
+                    *reinterpret_cast<uint4*>(row_at<T>(p.out, b, h, i) + c) = make_uint4(0, 0, 0, 0);
+            if (i < p.Tp) p.stats[row0 + i] = -CUDART_INF_F;
+        } else if (ok && wait.warp(smem_addr(&sh.done[x]), 0)) {
             tc_fence_after();
             const bool row = i < len;
             const float inv = row && l > 0.f ? 1.f / l : 0.f;
-            p.stats[(int64_t(b) * p.hq + h) * p.Tp + i] = row && l > 0.f ? -(m + __log2f(l)) : -CUDART_INF_F;
+            p.stats[row0 + i] = row && l > 0.f ? -(m + __log2f(l)) : -CUDART_INF_F;
             T* dst = row_at<T>(p.out, b, h, i);
+            uint8_t* low = p.low + (row0 + i) * kTile;
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                uint32_t o[32];
-                tmem_ld32(at + kFwdO + c * 32, o);
+                uint32_t o[32], hi[16], lo[8];
+                tmem_ld32(at + 256 + c * 32, o);
                 tmem_wait_ld();
+#pragma unroll
+                for (int z = 0; z < 32; z += 2) {
+                    const float2 y = make_float2(__uint_as_float(o[z]) * inv, __uint_as_float(o[z + 1]) * inv);
+                    hi[z / 2] = row ? Elem<T>::pack(y.x, y.y) : 0;
+                    const float2 w = Elem<T>::wide(hi[z / 2]);
+                    uint16_t f8;
+                    asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;"
+                        : "=h"(f8)
+                        : "f"((y.y - w.y) * kLowScale), "f"((y.x - w.x) * kLowScale));
+                    lo[z / 4] = z % 4 == 0 ? f8 : lo[z / 4] | uint32_t(f8) << 16;
+                }
                 if (i < p.T) {
 #pragma unroll
-                    for (int x = 0; x < 32; x += 8)
-                        *reinterpret_cast<uint4*>(dst + c * 32 + x) = row ? pack8<T>(o + x, inv) : make_uint4(0, 0, 0, 0);
+                    for (int z = 0; z < 4; ++z)
+                        *reinterpret_cast<uint4*>(dst + c * 32 + z * 8) =
+                            make_uint4(hi[4 * z], hi[4 * z + 1], hi[4 * z + 2], hi[4 * z + 3]);
+#pragma unroll
+                    for (int z = 0; z < 2; ++z)
+                        *reinterpret_cast<uint4*>(low + c * 32 + z * 16) =
+                            make_uint4(lo[4 * z], lo[4 * z + 1], lo[4 * z + 2], lo[4 * z + 3]);
                 }
             }
         }
     }
-    tc_fence_before();
-    __syncthreads();
-    if (warp == 1) {
-        tc_fence_after();
-        tmem_dealloc(tmem, kFwdCols);
-    }
+    tear_down(sh);
 }
 
 // ------------------------------------------------------------------ D_i = o_i . g_i
-// Bound by HBM: reads each output and gradient row once.  16 threads per row.
+// Bound by HBM: reads each output row, its remainder and the gradient's row
+// once; writes minus D.  The remainder matters where few keys share a row:
+// the rounding of o_i is then as large beside D_i as that of ds.  Sixteen
+// threads per row, four rows per thread.
+constexpr int kDeltaRows = 4;
+
 template <typename T>
 __global__ void __launch_bounds__(256) window_delta_kernel(const __grid_constant__ WindowAttnParams p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
-    const int64_t row = (int64_t(blockIdx.x) * 256 + threadIdx.x) / 16;
-    const int part = threadIdx.x % 16;
-    if (row >= int64_t(p.B) * p.hq * p.Tp) return;
-    const int64_t bh = row / p.Tp;
-    const int t = int(row - bh * p.Tp), b = int(bh / p.hq), h = int(bh - int64_t(b) * p.hq);
-    float d = 0.f;
-    if (t < length_of(p, b)) {
-        const uint4 x = *reinterpret_cast<const uint4*>(row_at<const T>(p.out, b, h, t) + part * 8);
-        const uint4 y = *reinterpret_cast<const uint4*>(row_at<const T>(p.dout, b, h, t) + part * 8);
-        const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+    // blockIdx.x: 64 rows of a (sequence, head); Tp is a multiple of 64
+    const int blocks = p.Tp / (16 * kDeltaRows), bh = int(blockIdx.x) / blocks, b = bh / p.hq, h = bh - b * p.hq;
+    const int t0 = (int(blockIdx.x) - bh * blocks) * (16 * kDeltaRows) + threadIdx.x / 16, part = threadIdx.x % 16;
+    const int len = length_of(p, b);
+    uint4 x[kDeltaRows], y[kDeltaRows];
+    uint2 lo[kDeltaRows];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float2 u = Elem<T>::wide(xs[k]), v = Elem<T>::wide(ys[k]);
-            d = fmaf(u.x, v.x, fmaf(u.y, v.y, d));
+    for (int k = 0; k < kDeltaRows; ++k) {
+        const int t = t0 + 16 * k;
+        x[k] = y[k] = make_uint4(0, 0, 0, 0);
+        lo[k] = make_uint2(0, 0);
+        if (t < len) {
+            x[k] = *reinterpret_cast<const uint4*>(row_at<const T>(p.out, b, h, t) + part * 8);
+            y[k] = *reinterpret_cast<const uint4*>(row_at<const T>(p.dout, b, h, t) + part * 8);
+            lo[k] = *reinterpret_cast<const uint2*>(p.low + (int64_t(bh) * p.Tp + t) * kTile + part * 8);
         }
     }
 #pragma unroll
-    for (int k = 8; k > 0; k >>= 1) d += __shfl_xor_sync(0xffffffffu, d, k);
-    if (part == 0) p.delta[row] = d;
+    for (int k = 0; k < kDeltaRows; ++k) {
+        const uint32_t xs[4] = {x[k].x, x[k].y, x[k].z, x[k].w}, ys[4] = {y[k].x, y[k].y, y[k].z, y[k].w};
+        float d = 0.f, rest = 0.f;
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+            const float2 u = Elem<T>::wide(xs[z]), v = Elem<T>::wide(ys[z]);
+            uint32_t f16;
+            asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(f16) : "h"(uint16_t((z < 2 ? lo[k].x : lo[k].y) >> (z % 2 * 16))));
+            const float2 w = __half22float2(*reinterpret_cast<const __half2*>(&f16));
+            d = fmaf(u.x, v.x, fmaf(u.y, v.y, d));
+            rest = fmaf(w.x, v.x, fmaf(w.y, v.y, rest));
+        }
+        d = fmaf(rest, 1.f / kLowScale, d);
+#pragma unroll
+        for (int z = 8; z > 0; z >>= 1) d += __shfl_xor_sync(0xffffffffu, d, z);
+        if (part == 0) p.delta[int64_t(bh) * p.Tp + t0 + 16 * k] = -d;
+    }
 }
 
 // ------------------------------------------------------------------ backward
-// 10 warps: 0-7 elementwise (two per TMEM lane quarter, one 64-column half
-// each), 8 TMA, 9 products.  One launch holds two kinds of work items: first
-// those of the key tiles (the longest), then those of the query tiles, which
-// fill the SMs that have run out of the first.
-constexpr int kBwdThreads = 320;
-constexpr uint32_t kBwdSmem = 6 * kTileBytes + 4 * kTile * 4 + 1024;
-constexpr uint32_t kBwdCols = 512;
-
-struct BwdShared {
-    uint64_t once, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full, dp_full, ds_full, done;
-    uint32_t tmem;
-    int abort_flag;
-};
+// One launch holds two kinds of work items: first those of the key tiles (the
+// longest), then those of the query tiles, which fill the SMs that have run
+// out of the first.  Warps 0-7: two per TMEM lane quarter, one 64-column half
+// each.
 
 // What a key tile's work item is: rows x of its list of (query head of the
 // group, query tile), x0 <= x < x1.
@@ -484,118 +616,129 @@ struct KeyItem {
     }
 };
 
-// Key tile: K, V stay; Q and g tiles pass.  With keys along the TMEM lanes,
-//   S^T = K Q^T, P^T = exp2(..) over S^T,  dP^T = V g^T, dS^T over dP^T,
-//   dV += P^T g,  dK += dS^T Q
-// P^T and dS^T are the A operands of the second pair straight from TMEM.
-// The products of one phase run under the elementwise work of the other:
-// dV_x and S_{x+1} while dS_x is worked out, dK_x and dP_{x+1} while P_{x+1} is.
+// Key tile: K, V stay; Q (a ring of three) and g (of two) pass.  With keys
+// along the TMEM lanes,
+//   S^T = K Q^T, P^T = exp2(..),  dP^T = V g^T, dS^T = P^T (dP^T - D),
+//   dV += P^T g,  dK += dS^T Q,
+// P^T and dS^T being A operands straight from TMEM.  S^T and dP^T take turns
+// in one TMEM region: as soon as one is in registers the other's product
+// starts, so that dP_x is worked out under the exponentials of S_x and S_{x+1}
+// under dS_x; dK_{x-1} and dV_x fill the rest.
 template <typename T>
-__device__ __forceinline__ void key_tile(const WindowAttnParams& p, BwdShared& sh, uint32_t smem, const Waiter& wait) {
+__device__ __forceinline__ void key_tile(const WindowAttnParams& p, Bars& sh, uint32_t smem, const Waiter& wait) {
     constexpr uint32_t kDims = idesc_f16(kTile, kTile, Elem<T>::bf16, false, false);
     constexpr uint32_t kRows = idesc_f16(kTile, kTile, Elem<T>::bf16, false, true);
-    constexpr uint32_t kS = 0, kDP = 128, kDV = 256, kDK = 384;
+    constexpr uint32_t kA = 0, kP = 128, kDS = 192, kDV = 256, kDK = 384;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const KeyItem it(p, int(blockIdx.x));
-    const uint32_t sK = smem, sV = sK + kTileBytes, sQ = sV + kTileBytes, sG = sQ + 2 * kTileBytes,
-                   sStat = sG + 2 * kTileBytes;       // [stage][stats, delta][128]
+    const uint32_t sK = smem, sV = sK + kTileBytes, sQ = sV + kTileBytes, sG = sQ + kRing3 * kTileBytes;
+    const uint32_t sStat = smem + kStatsAt, sDelta = sStat + kRing3 * kTile * 4;
     const int len = length_of(p, it.b), k0 = it.kt * kTile, n = it.x1 - it.x0;
     const uint32_t tmem = sh.tmem;
+    // whether the sequence ends inside query tile x of the list: its Q and g
+    // are zeroed behind the end before any product reads them
+    const auto cut = [&](int x) {
+        const int i0 = (it.kt + (it.x0 + x) % it.nq) * kTile;
+        return i0 + kTile > len && len < p.T;
+    };
 
     if (warp == 8) {
         if (lane == 0 && n > 0) {
             mbar_arrive_expect_tx(smem_addr(&sh.once), 2 * kTileBytes);
             tma_tile(sK, &p.tm_k, k0, it.g, it.b, smem_addr(&sh.once));
             tma_tile(sV, &p.tm_v, k0, it.g, it.b, smem_addr(&sh.once));
-            int x = 0;
-            for (; x < n; ++x) {
-                const int st = x & 1, at = it.x0 + x;
-                const int h = it.g * p.G + at / it.nq, i0 = (it.kt + at % it.nq) * kTile;
-                const uint32_t bar = smem_addr(&sh.k_full[st]);
-                if (!wait.timed(smem_addr(&sh.k_empty[st]), ((x >> 1) & 1) ^ 1)) break;
-                mbar_arrive_expect_tx(bar, 2 * kTileBytes + 2 * kTile * 4);
-                tma_tile(sQ + st * kTileBytes, &p.tm_q, i0, h, it.b, bar);
-                tma_tile(sG + st * kTileBytes, &p.tm_do, i0, h, it.b, bar);
+            int qs = 0, gs = 0;
+            for (int x = 0; x < n; ++x) {
+                const int at = it.x0 + x, h = it.g * p.G + at / it.nq, i0 = (it.kt + at % it.nq) * kTile;
                 const int64_t row = (int64_t(it.b) * p.hq + h) * p.Tp + i0;
-                bulk_row(sStat + st * kTile * 8, p.stats + row, bar);
-                bulk_row(sStat + st * kTile * 8 + kTile * 4, p.delta + row, bar);
+                const int q3 = x % kRing3, g2 = x % kRing2;
+                uint32_t bar = smem_addr(&sh.full3[q3]);
+                if (!wait.thread(smem_addr(&sh.empty3[q3]), ((x / kRing3) & 1) ^ 1)) break;
+                mbar_arrive_expect_tx(bar, kTileBytes + kTile * 4);
+                tma_tile(sQ + q3 * kTileBytes, &p.tm_q, i0, h, it.b, bar);
+                bulk_row(sStat + q3 * kTile * 4, p.stats + row, bar);
+                ++qs;
+                bar = smem_addr(&sh.full2[g2]);
+                if (!wait.thread(smem_addr(&sh.empty2[g2]), ((x / kRing2) & 1) ^ 1)) break;
+                mbar_arrive_expect_tx(bar, kTileBytes + kTile * 4);
+                tma_tile(sG + g2 * kTileBytes, &p.tm_do, i0, h, it.b, bar);
+                bulk_row(sDelta + g2 * kTile * 4, p.delta + row, bar);
+                ++gs;
             }
             mbar_wait(smem_addr(&sh.once), 0, p.timeout_ns);
-            for (int k = 1; k <= 2 && k <= x; ++k)
-                mbar_wait(smem_addr(&sh.k_full[(x - k) & 1]), ((x - k) >> 1) & 1, p.timeout_ns);
+            drain<kRing3>(sh.full3, qs, p.timeout_ns);
+            drain<kRing2>(sh.full2, gs, p.timeout_ns);
         }
     } else if (warp == 9) {
-        bool ok = n > 0 && wait.warp(smem_addr(&sh.once), 0);
-        // Q and g of step x, without what lies behind the sequence
-        const auto arrived = [&](int x) {
-            const int st = x & 1, i0 = (it.kt + (it.x0 + x) % it.nq) * kTile;
-            if (!wait.warp(smem_addr(&sh.k_full[st]), (x >> 1) & 1)) return false;
-            if (i0 + kTile > len && len < p.T) {
-                zero_rows(sQ + st * kTileBytes, len - i0);
-                zero_rows(sG + st * kTileBytes, len - i0);
-            }
-            return true;
-        };
-        if (ok) ok = arrived(0);
-        if (ok && lane == 0) {
-            mma_dims(tmem + kS, sK, sQ, kDims);
-            umma_commit(smem_addr(&sh.s_full[0]));
-            mma_dims(tmem + kDP, sV, sG, kDims);
-            umma_commit(smem_addr(&sh.dp_full));
-        }
-        __syncwarp();
-        for (int x = 0; ok && x < n; ++x) {
-            const int st = x & 1, nx = st ^ 1;
-            const bool more = x + 1 < n;
-            ok = wait.warp(smem_addr(&sh.p_full), x & 1);
-            if (!ok) break;
-            tc_fence_after();
-            if (lane == 0) mma_rows(tmem + kDV, tmem + kS, 64, sG + st * kTileBytes, kRows, x > 0);
-            __syncwarp();
-            if (more) {
-                ok = arrived(x + 1);
-                if (!ok) break;
-                if (lane == 0) {
-                    mma_dims(tmem + kS, sK, sQ + nx * kTileBytes, kDims);
-                    umma_commit(smem_addr(&sh.s_full[0]));
-                }
-                __syncwarp();
-            }
-            ok = wait.warp(smem_addr(&sh.ds_full), x & 1);
-            if (!ok) break;
-            tc_fence_after();
-            if (lane == 0) {
-                mma_rows(tmem + kDK, tmem + kDP, 64, sQ + st * kTileBytes, kRows, x > 0);
-                umma_commit(smem_addr(&sh.k_empty[st]));
-                if (more) {
-                    mma_dims(tmem + kDP, sV, sG + nx * kTileBytes, kDims);
-                    umma_commit(smem_addr(&sh.dp_full));
-                }
-            }
-            __syncwarp();
-        }
         if (lane == 0) {
-            umma_commit(smem_addr(&sh.done));
-            mbar_wait(smem_addr(&sh.done), 0, p.timeout_ns);
+            bool ok = n > 0 && wait.thread(smem_addr(&sh.once), 0);
+            int trims = 0;
+            const auto scores = [&](int x) {
+                if (!wait.thread(smem_addr(&sh.full3[x % kRing3]), (x / kRing3) & 1)) return false;
+                if (cut(x) && !wait.thread(smem_addr(&sh.trimmed), trims++ & 1)) return false;
+                mma_dims(tmem + kA, sK, sQ + x % kRing3 * kTileBytes, kDims);
+                umma_commit(smem_addr(&sh.s_full[0]));
+                return true;
+            };
+            const auto keys_grad = [&](int x) {
+                if (!wait.thread(smem_addr(&sh.ds_full), x & 1)) return false;
+                tc_fence_after();
+                mma_rows(tmem + kDK, tmem + kDS, 32, sQ + x % kRing3 * kTileBytes, kRows, x > 0);
+                umma_commit(smem_addr(&sh.empty3[x % kRing3]));
+                return true;
+            };
+            ok = ok && scores(0);
+            for (int x = 0; ok && x < n; ++x) {
+                const uint32_t tile = sG + x % kRing2 * kTileBytes;
+                ok = wait.thread(smem_addr(&sh.full2[x % kRing2]), (x / kRing2) & 1) &&
+                     wait.thread(smem_addr(&sh.s_read), x & 1);
+                if (!ok) break;
+                tc_fence_after();
+                mma_dims(tmem + kA, sV, tile, kDims);
+                umma_commit(smem_addr(&sh.dp_full));
+                if (x > 0) ok = keys_grad(x - 1);
+                ok = ok && wait.thread(smem_addr(&sh.dp_read), x & 1);
+                if (!ok) break;
+                tc_fence_after();
+                if (x + 1 < n) ok = scores(x + 1);
+                ok = ok && wait.thread(smem_addr(&sh.p_full[0]), x & 1);
+                if (!ok) break;
+                tc_fence_after();
+                mma_rows(tmem + kDV, tmem + kP, 32, tile, kRows, x > 0);
+                umma_commit(smem_addr(&sh.empty2[x % kRing2]));
+            }
+            if (ok && n > 0) keys_grad(n - 1);
+            umma_commit(smem_addr(&sh.done[0]));
+            mbar_wait(smem_addr(&sh.done[0]), 0, p.timeout_ns);
         }
         __syncwarp();
     } else {
         const int quarter = warp & 3, half = warp >> 2, r = quarter * 32 + lane, key = k0 + r, cb = half * 64;
-        const uint32_t at = tmem + (uint32_t(quarter * 32) << 16) + cb;
+        const uint32_t at = tmem + (uint32_t(quarter * 32) << 16);
         const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
         bool ok = true;
         for (int x = 0; x < n; ++x) {
-            const int st = x & 1, qt = it.kt + (it.x0 + x) % it.nq, i0 = qt * kTile;
-            const uint32_t stat = sStat + st * kTile * 8 + cb * 4;
-            // this thread's own wait for the statistics that came with Q and g
-            ok = wait.warp(smem_addr(&sh.k_full[st]), (x >> 1) & 1) && wait.warp(smem_addr(&sh.s_full[0]), x & 1);
+            const int qt = it.kt + (it.x0 + x) % it.nq, i0 = qt * kTile;
+            const uint32_t stat = sStat + x % kRing3 * kTile * 4 + cb * 4, delta = sDelta + x % kRing2 * kTile * 4 + cb * 4;
+            // the statistics came with Q, D with g: this warp's own waits for them
+            ok = wait.warp(smem_addr(&sh.full3[x % kRing3]), (x / kRing3) & 1);
+            if (!ok) break;
+            if (cut(x)) {
+                ok = wait.warp(smem_addr(&sh.full2[x % kRing2]), (x / kRing2) & 1);
+                if (!ok) break;
+                zero_rows(sQ + x % kRing3 * kTileBytes, len - i0, warp, 8);
+                zero_rows(sG + x % kRing2 * kTileBytes, len - i0, warp, 8);
+                arrive_warp(&sh.trimmed);
+            }
+            ok = wait.warp(smem_addr(&sh.s_full[0]), x & 1);
             if (!ok) break;
             tc_fence_after();
             float s[64];
             uint32_t* u = reinterpret_cast<uint32_t*>(s);
-            tmem_ld32p(at + kS, u);
-            tmem_ld32p(at + kS + 32, u + 32);
+            tmem_ld32p(at + kA + cb, u);
+            tmem_ld32p(at + kA + cb + 32, u + 32);
             tmem_wait_ld();
+            arrive_warp(&sh.s_read);
             if (qt == it.kt || !whole(p, qt, it.kt) || i0 + kTile > len) {
                 // rows i0 + c with key <= row < len, within the window unless the key is a sink
                 int hi = len - 1 - i0;
@@ -608,108 +751,102 @@ __device__ __forceinline__ void key_tile(const WindowAttnParams& p, BwdShared& s
                     for (int c = 0; c < 32; ++c) s[q * 32 + c] = (keep >> c) & 1u ? s[q * 32 + c] : -CUDART_INF_F;
                 }
             }
+            uint32_t ph[32];
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                uint32_t ph[16];
-#pragma unroll
-                for (int c = 0; c < 32; c += 4) {
-                    const uint4 nl = lds128(stat + (q * 32 + c) * 4);
-                    float* e = s + q * 32 + c;
-                    const float2 a = ffma2(make_float2(e[0], e[1]), sc2,
-                                           make_float2(__uint_as_float(nl.x), __uint_as_float(nl.y)));
-                    const float2 d = ffma2(make_float2(e[2], e[3]), sc2,
-                                           make_float2(__uint_as_float(nl.z), __uint_as_float(nl.w)));
-                    e[0] = fast_exp2(a.x);
-                    e[1] = fast_exp2(a.y);
-                    e[2] = fast_exp2(d.x);
-                    e[3] = fast_exp2(d.y);
-                    ph[c / 2] = Elem<T>::pack(e[0], e[1]);
-                    ph[c / 2 + 1] = Elem<T>::pack(e[2], e[3]);
-                }
-                tmem_stn<16>(at + kS + q * 16, ph);     // over this thread's own columns of S^T
+            for (int c = 0; c < 64; c += 4) {
+                const uint4 nl = lds128(stat + c * 4);
+                float* e = s + c;
+                const float2 y = ffma2(make_float2(e[0], e[1]), sc2,
+                                       make_float2(__uint_as_float(nl.x), __uint_as_float(nl.y)));
+                const float2 z = ffma2(make_float2(e[2], e[3]), sc2,
+                                       make_float2(__uint_as_float(nl.z), __uint_as_float(nl.w)));
+                e[0] = fast_exp2(y.x);
+                e[1] = fast_exp2(y.y);
+                e[2] = fast_exp2(z.x);
+                e[3] = fast_exp2(z.y);
+                ph[c / 2] = Elem<T>::pack(e[0], e[1]);
+                ph[c / 2 + 1] = Elem<T>::pack(e[2], e[3]);
             }
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_addr(&sh.p_full));
-            ok = wait.warp(smem_addr(&sh.dp_full), x & 1);
+            // P_{x-1} has been used
+            if (x > 0) ok = wait.warp(smem_addr(&sh.empty2[(x - 1) % kRing2]), ((x - 1) / kRing2) & 1);
             if (!ok) break;
             tc_fence_after();
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                uint32_t d[32], ph[16];
-                tmem_ld32(at + kDP + q * 32, d);
-                tmem_wait_ld();
-#pragma unroll
-                for (int c = 0; c < 32; c += 4) {
-                    const uint4 dl = lds128(stat + kTile * 4 + (q * 32 + c) * 4);
-                    const float* e = s + q * 32 + c;
-                    ph[c / 2] = Elem<T>::pack(e[0] * (__uint_as_float(d[c]) - __uint_as_float(dl.x)),
-                                              e[1] * (__uint_as_float(d[c + 1]) - __uint_as_float(dl.y)));
-                    ph[c / 2 + 1] = Elem<T>::pack(e[2] * (__uint_as_float(d[c + 2]) - __uint_as_float(dl.z)),
-                                                  e[3] * (__uint_as_float(d[c + 3]) - __uint_as_float(dl.w)));
-                }
-                // over columns 0..31, which this thread has read
-                tmem_stn<16>(at + kDP + q * 16, ph);
-            }
+            tmem_stn<32>(at + kP + half * 32, ph);
             tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_addr(&sh.ds_full));
+            arrive_warp(&sh.p_full[0]);
+            ok = wait.warp(smem_addr(&sh.full2[x % kRing2]), (x / kRing2) & 1) && wait.warp(smem_addr(&sh.dp_full), x & 1);
+            if (!ok) break;
+            tc_fence_after();
+            uint32_t d[64];
+            tmem_ld32p(at + kA + cb, d);
+            tmem_ld32p(at + kA + cb + 32, d + 32);
+            tmem_wait_ld();
+            arrive_warp(&sh.dp_read);
+#pragma unroll
+            for (int c = 0; c < 64; c += 4) {
+                const uint4 dl = lds128(delta + c * 4);
+                const float* e = s + c;
+                const float2 y = fmul2(make_float2(e[0], e[1]),
+                                       fadd2(make_float2(__uint_as_float(d[c]), __uint_as_float(d[c + 1])),
+                                             make_float2(__uint_as_float(dl.x), __uint_as_float(dl.y))));
+                const float2 z = fmul2(make_float2(e[2], e[3]),
+                                       fadd2(make_float2(__uint_as_float(d[c + 2]), __uint_as_float(d[c + 3])),
+                                             make_float2(__uint_as_float(dl.z), __uint_as_float(dl.w))));
+                ph[c / 2] = Elem<T>::pack(y.x, y.y);
+                ph[c / 2 + 1] = Elem<T>::pack(z.x, z.y);
+            }
+            // dS_{x-1} has been used
+            if (x > 0) ok = wait.warp(smem_addr(&sh.empty3[(x - 1) % kRing3]), ((x - 1) / kRing3) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            tmem_stn<32>(at + kDS + half * 32, ph);
+            tmem_wait_st();
+            arrive_warp(&sh.ds_full);
         }
-        if (ok) ok = wait.warp(smem_addr(&sh.done), 0);
+        if (ok) ok = wait.warp(smem_addr(&sh.done[0]), 0);
         if (ok) {
             tc_fence_after();
             const bool row = key < len && n > 0;
-            if (it.pieces > 1) {
-                float* dst = p.part + it.slot * (2 * kTile * kTile) + r * kTile + cb;
 #pragma unroll
-                for (int w = 0; w < 2; ++w)
+            for (int w = 0; w < 2; ++w)
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        uint32_t o[32];
-                        tmem_ld32(at + (w ? kDV : kDK) + c * 32, o);
-                        tmem_wait_ld();
-                        float4* y = reinterpret_cast<float4*>(dst + w * kTile * kTile + c * 32);
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t o[32];
+                    tmem_ld32(at + (w ? kDV : kDK) + cb + c * 32, o);
+                    tmem_wait_ld();
+                    if (it.pieces > 1) {
+                        float4* y = reinterpret_cast<float4*>(p.part + it.slot * (2 * kTile * kTile) + w * kTile * kTile +
+                                                              r * kTile + cb + c * 32);
 #pragma unroll
                         for (int z = 0; z < 32; z += 4)
                             y[z / 4] = row ? make_float4(__uint_as_float(o[z]), __uint_as_float(o[z + 1]),
                                                          __uint_as_float(o[z + 2]), __uint_as_float(o[z + 3]))
                                            : make_float4(0.f, 0.f, 0.f, 0.f);
+                    } else if (key < p.T) {
+                        T* dst = row_at<T>(w ? p.dv : p.dk, it.b, it.g, key) + cb + c * 32;
+#pragma unroll
+                        for (int z = 0; z < 32; z += 8)
+                            *reinterpret_cast<uint4*>(dst + z) = row ? pack8<T>(o + z, w ? 1.f : p.scale) : make_uint4(0, 0, 0, 0);
                     }
-            } else {
-#pragma unroll
-                for (int w = 0; w < 2; ++w)
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        uint32_t o[32];
-                        tmem_ld32(at + (w ? kDV : kDK) + c * 32, o);
-                        tmem_wait_ld();
-                        if (key < p.T) {
-                            T* dst = row_at<T>(w ? p.dv : p.dk, it.b, it.g, key) + cb + c * 32;
-#pragma unroll
-                            for (int z = 0; z < 32; z += 8)
-                                *reinterpret_cast<uint4*>(dst + z) =
-                                    row ? pack8<T>(o + z, w ? 1.f : p.scale) : make_uint4(0, 0, 0, 0);
-                        }
-                    }
-            }
+                }
         }
     }
 }
 
-// Query tile: Q, g stay; K and V tiles pass.  With rows along the TMEM lanes,
-//   S = Q K^T (two buffers), dP = g V^T, dS over S, dQ += dS K.
+// Query tile: Q, g stay; K (a ring of three) and V (of two) pass.  With rows
+// along the TMEM lanes,
+//   S = Q K^T (two regions), dP = g V^T, dS over S, dQ += dS K.
+// S_{j+1} is worked out under the exponentials of S_j, dP_{j+1} as soon as
+// dP_j is in registers.
 template <typename T>
-__device__ __forceinline__ void query_tile(const WindowAttnParams& p, BwdShared& sh, uint32_t smem,
-                                           const Waiter& wait) {
+__device__ __forceinline__ void query_tile(const WindowAttnParams& p, Bars& sh, uint32_t smem, const Waiter& wait) {
     constexpr uint32_t kDims = idesc_f16(kTile, kTile, Elem<T>::bf16, false, false);
     constexpr uint32_t kRows = idesc_f16(kTile, kTile, Elem<T>::bf16, false, true);
     constexpr uint32_t kS = 0, kDP = 256, kDQ = 384;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int item = int(blockIdx.x) - p.items_kv, heads = p.B * p.hq;
     const int qt = p.n_t - 1 - item / heads, b = item % heads / p.hq, h = item % p.hq, g = h / p.G;
-    const uint32_t sQ = smem, sG = sQ + kTileBytes, sK = sG + kTileBytes, sV = sK + 2 * kTileBytes;
+    const uint32_t sQ = smem, sG = sQ + kTileBytes, sK = sG + kTileBytes, sV = sK + kRing3 * kTileBytes;
     const int len = length_of(p, b), i0 = qt * kTile;
     const KeyTiles tiles(p, qt);
     const int n = i0 < len ? tiles.n : 0;
@@ -723,65 +860,52 @@ __device__ __forceinline__ void query_tile(const WindowAttnParams& p, BwdShared&
             tma_tile(sG, &p.tm_do, i0, h, b, smem_addr(&sh.once));
             int ks = 0, vs = 0;
             for (int j = 0; j < n; ++j) {
-                const int st = j & 1, t = tiles.at(j) * kTile;
-                const uint32_t parity = ((j >> 1) & 1) ^ 1;
-                if (!wait.timed(smem_addr(&sh.k_empty[st]), parity)) break;
-                mbar_arrive_expect_tx(smem_addr(&sh.k_full[st]), kTileBytes);
-                tma_tile(sK + st * kTileBytes, &p.tm_k, t, g, b, smem_addr(&sh.k_full[st]));
+                const int k3 = j % kRing3, v2 = j % kRing2, t = tiles.at(j) * kTile;
+                if (!wait.thread(smem_addr(&sh.empty3[k3]), ((j / kRing3) & 1) ^ 1)) break;
+                mbar_arrive_expect_tx(smem_addr(&sh.full3[k3]), kTileBytes);
+                tma_tile(sK + k3 * kTileBytes, &p.tm_k, t, g, b, smem_addr(&sh.full3[k3]));
                 ++ks;
-                if (!wait.timed(smem_addr(&sh.v_empty[st]), parity)) break;
-                mbar_arrive_expect_tx(smem_addr(&sh.v_full[st]), kTileBytes);
-                tma_tile(sV + st * kTileBytes, &p.tm_v, t, g, b, smem_addr(&sh.v_full[st]));
+                if (!wait.thread(smem_addr(&sh.empty2[v2]), ((j / kRing2) & 1) ^ 1)) break;
+                mbar_arrive_expect_tx(smem_addr(&sh.full2[v2]), kTileBytes);
+                tma_tile(sV + v2 * kTileBytes, &p.tm_v, t, g, b, smem_addr(&sh.full2[v2]));
                 ++vs;
             }
             mbar_wait(smem_addr(&sh.once), 0, p.timeout_ns);
-            for (int k = 1; k <= 2 && k <= ks; ++k)
-                mbar_wait(smem_addr(&sh.k_full[(ks - k) & 1]), ((ks - k) >> 1) & 1, p.timeout_ns);
-            for (int k = 1; k <= 2 && k <= vs; ++k)
-                mbar_wait(smem_addr(&sh.v_full[(vs - k) & 1]), ((vs - k) >> 1) & 1, p.timeout_ns);
+            drain<kRing3>(sh.full3, ks, p.timeout_ns);
+            drain<kRing2>(sh.full2, vs, p.timeout_ns);
         }
     } else if (warp == 9) {
-        bool ok = n > 0 && wait.warp(smem_addr(&sh.once), 0);
-        const auto keys = [&](int j) {
-            const uint32_t tile = sK + (j & 1) * kTileBytes;
-            if (!wait.warp(smem_addr(&sh.k_full[j & 1]), (j >> 1) & 1)) return false;
-            if (cut && j == n - 1) zero_rows(tile, len - i0);
-            if (lane == 0) {
-                mma_dims(tmem + kS + (j & 1) * 128, sQ, tile, kDims);
-                umma_commit(smem_addr(&sh.s_full[j & 1]));
-            }
-            __syncwarp();
-            return true;
-        };
-        const auto values = [&](int j) {
-            const uint32_t tile = sV + (j & 1) * kTileBytes;
-            if (!wait.warp(smem_addr(&sh.v_full[j & 1]), (j >> 1) & 1)) return false;
-            if (cut && j == n - 1) zero_rows(tile, len - i0);
-            if (lane == 0) {
-                mma_dims(tmem + kDP, sG, tile, kDims);
-                umma_commit(smem_addr(&sh.dp_full));
-                umma_commit(smem_addr(&sh.v_empty[j & 1]));
-            }
-            __syncwarp();
-            return true;
-        };
-        ok = ok && keys(0) && values(0);
-        for (int j = 0; ok && j < n; ++j) {
-            if (j + 1 < n) ok = keys(j + 1);
-            ok = ok && wait.warp(smem_addr(&sh.ds_full), j & 1);
-            if (!ok) break;
-            tc_fence_after();
-            if (j + 1 < n) ok = values(j + 1);
-            if (!ok) break;
-            if (lane == 0) {
-                mma_rows(tmem + kDQ, tmem + kS + (j & 1) * 128, 64, sK + (j & 1) * kTileBytes, kRows, j > 0);
-                umma_commit(smem_addr(&sh.k_empty[j & 1]));
-            }
-            __syncwarp();
-        }
         if (lane == 0) {
-            umma_commit(smem_addr(&sh.done));
-            mbar_wait(smem_addr(&sh.done), 0, p.timeout_ns);
+            bool ok = n > 0 && wait.thread(smem_addr(&sh.once), 0);
+            const auto keys = [&](int j) {
+                if (!wait.thread(smem_addr(&sh.full3[j % kRing3]), (j / kRing3) & 1)) return false;
+                if (cut && j == n - 1 && !wait.thread(smem_addr(&sh.trimmed), 0)) return false;
+                mma_dims(tmem + kS + (j & 1) * 128, sQ, sK + j % kRing3 * kTileBytes, kDims);
+                umma_commit(smem_addr(&sh.s_full[j & 1]));
+                return true;
+            };
+            const auto values = [&](int j) {
+                if (!wait.thread(smem_addr(&sh.full2[j % kRing2]), (j / kRing2) & 1)) return false;
+                mma_dims(tmem + kDP, sG, sV + j % kRing2 * kTileBytes, kDims);
+                umma_commit(smem_addr(&sh.dp_full));
+                umma_commit(smem_addr(&sh.empty2[j % kRing2]));
+                return true;
+            };
+            ok = ok && keys(0) && values(0);
+            for (int j = 0; ok && j < n; ++j) {
+                if (j + 1 < n) ok = keys(j + 1);
+                ok = ok && wait.thread(smem_addr(&sh.dp_read), j & 1);
+                if (!ok) break;
+                tc_fence_after();
+                if (j + 1 < n) ok = values(j + 1);
+                ok = ok && wait.thread(smem_addr(&sh.ds_full), j & 1);
+                if (!ok) break;
+                tc_fence_after();
+                mma_rows(tmem + kDQ, tmem + kS + (j & 1) * 128, 64, sK + j % kRing3 * kTileBytes, kRows, j > 0);
+                umma_commit(smem_addr(&sh.empty3[j % kRing3]));
+            }
+            umma_commit(smem_addr(&sh.done[0]));
+            mbar_wait(smem_addr(&sh.done[0]), 0, p.timeout_ns);
         }
         __syncwarp();
     } else {
@@ -789,11 +913,20 @@ __device__ __forceinline__ void query_tile(const WindowAttnParams& p, BwdShared&
         const uint32_t at = tmem + (uint32_t(quarter * 32) << 16) + cb;
         const int64_t row = (int64_t(b) * p.hq + h) * p.Tp + i;
         const float nl = p.stats[row], dl = p.delta[row];
-        const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nl2 = make_float2(nl, nl);
+        const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nl2 = make_float2(nl, nl), dl2 = make_float2(dl, dl);
         bool ok = true;
         for (int j = 0; j < n; ++j) {
             const int kt = tiles.at(j);
             const uint32_t sb = kS + (j & 1) * 128;
+            if (cut && j == n - 1) {
+                // the sequence ends inside its last key tile; j - 1's products have used the rings' phases before
+                ok = wait.warp(smem_addr(&sh.full3[j % kRing3]), (j / kRing3) & 1) &&
+                     wait.warp(smem_addr(&sh.full2[j % kRing2]), (j / kRing2) & 1);
+                if (!ok) break;
+                zero_rows(sK + j % kRing3 * kTileBytes, len - i0, warp, 8);
+                zero_rows(sV + j % kRing2 * kTileBytes, len - i0, warp, 8);
+                arrive_warp(&sh.trimmed);
+            }
             ok = wait.warp(smem_addr(&sh.s_full[j & 1]), (j >> 1) & 1);
             if (!ok) break;
             tc_fence_after();
@@ -812,30 +945,29 @@ __device__ __forceinline__ void query_tile(const WindowAttnParams& p, BwdShared&
             }
 #pragma unroll
             for (int c = 0; c < 64; c += 2) {
-                const float2 a = ffma2(make_float2(s[c], s[c + 1]), sc2, nl2);
-                s[c] = fast_exp2(a.x);
-                s[c + 1] = fast_exp2(a.y);
+                const float2 y = ffma2(make_float2(s[c], s[c + 1]), sc2, nl2);
+                s[c] = fast_exp2(y.x);
+                s[c + 1] = fast_exp2(y.y);
             }
             ok = wait.warp(smem_addr(&sh.dp_full), j & 1);
             if (!ok) break;
             tc_fence_after();
+            uint32_t d[64], ph[32];
+            tmem_ld32p(at + kDP, d);
+            tmem_ld32p(at + kDP + 32, d + 32);
+            tmem_wait_ld();
+            arrive_warp(&sh.dp_read);
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                uint32_t d[32], ph[16];
-                tmem_ld32(at + kDP + q * 32, d);
-                tmem_wait_ld();
-#pragma unroll
-                for (int c = 0; c < 32; c += 2)
-                    ph[c / 2] = Elem<T>::pack(s[q * 32 + c] * (__uint_as_float(d[c]) - dl),
-                                              s[q * 32 + c + 1] * (__uint_as_float(d[c + 1]) - dl));
-                tmem_stn<16>(at + sb + q * 16, ph);     // over this thread's own columns of S
+            for (int c = 0; c < 64; c += 2) {
+                const float2 y = fmul2(make_float2(s[c], s[c + 1]),
+                                       fadd2(make_float2(__uint_as_float(d[c]), __uint_as_float(d[c + 1])), dl2));
+                ph[c / 2] = Elem<T>::pack(y.x, y.y);
             }
+            tmem_stn<32>(at + sb, ph);     // over this thread's own columns of S
             tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_addr(&sh.ds_full));
+            arrive_warp(&sh.ds_full);
         }
-        if (ok) ok = wait.warp(smem_addr(&sh.done), 0);
+        if (ok) ok = wait.warp(smem_addr(&sh.done[0]), 0);
         if (ok) {
             tc_fence_after();
 #pragma unroll
@@ -856,25 +988,15 @@ __device__ __forceinline__ void query_tile(const WindowAttnParams& p, BwdShared&
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kBwdThreads, 1) window_bwd_kernel(const __grid_constant__ WindowAttnParams p) {
-    extern __shared__ unsigned char smem_raw[];
-    __shared__ __align__(8) BwdShared sh;
-    const uint32_t smem = (smem_addr(smem_raw) + 1023) & ~1023u;
-    const int warp = threadIdx.x >> 5;
-    if (threadIdx.x == 0) {
-        for (uint64_t* bar : {&sh.once, &sh.k_full[0], &sh.k_full[1], &sh.k_empty[0], &sh.k_empty[1], &sh.v_full[0],
-                              &sh.v_full[1], &sh.v_empty[0], &sh.v_empty[1], &sh.s_full[0], &sh.s_full[1],
-                              &sh.dp_full, &sh.done})
-            mbar_init(smem_addr(bar), 1);
-        mbar_init(smem_addr(&sh.p_full), 8);
-        mbar_init(smem_addr(&sh.ds_full), 8);
-        sh.abort_flag = 0;
-        fence_mbar_init();
+__global__ void __launch_bounds__(kThreads, 1) window_bwd_kernel(const __grid_constant__ WindowAttnParams p) {
+    extern __shared__ __align__(1024) unsigned char raw[];
+    Bars& sh = bars_of(raw);
+    const uint32_t smem = smem_addr(raw);
+    if (smem & 1023u) {
+        if (p.status && threadIdx.x == 0) set_status(p.status, DUO_STATUS_WAIT_TIMEOUT);
+        return;
     }
-    if (warp == 9) tmem_alloc(smem_addr(&sh.tmem), kBwdCols);
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
+    set_up(sh, 8);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     const Waiter wait{p.status, p.timeout_ns, &sh.abort_flag};
@@ -882,12 +1004,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) window_bwd_kernel(const __grid
         key_tile<T>(p, sh, smem, wait);
     else
         query_tile<T>(p, sh, smem, wait);
-    tc_fence_before();
-    __syncthreads();
-    if (warp == 9) {
-        tc_fence_after();
-        tmem_dealloc(sh.tmem, kBwdCols);
-    }
+    tear_down(sh);
 }
 
 // dK, dV of the key tiles whose rows were shared out: the pieces' sums, in
@@ -969,7 +1086,9 @@ int check_heads(const duo_heads* x, const duo_window_attn_desc& d, int heads) {
 
 HeadTensor head_tensor(const duo_heads& x) { return HeadTensor{x.data, x.batch_stride, x.head_stride, x.token_stride}; }
 
-void fill_params(WindowAttnParams& p, const duo_window_attn_desc& d, int32_t* status) {
+void fill_params(WindowAttnParams& p, const duo_window_attn_desc& d, float* stats, int32_t* status) {
+    p.stats = stats;
+    p.low = reinterpret_cast<uint8_t*>(stats + int64_t(d.batch) * d.num_q_heads * padded(d.tokens));
     p.B = d.batch;
     p.hq = d.num_q_heads;
     p.n_kv = d.num_kv_heads;
@@ -1052,17 +1171,17 @@ cudaError_t launch(K kernel, const WindowAttnParams& p, dim3 grid, int threads, 
 
 template <typename T>
 int run_forward(const WindowAttnParams& p, cudaStream_t s) {
-    return launch(window_fwd_kernel<T>, p, dim3(unsigned(p.n_t * p.B * p.hq)), kFwdThreads, kFwdSmem, s) == cudaSuccess
+    return launch(window_fwd_kernel<T>, p, dim3(unsigned((p.n_t + 1) / 2 * p.B * p.hq)), kThreads, kSmem, s) == cudaSuccess
                ? DUO_OK
                : DUO_ERR_CUDA;
 }
 
 template <typename T>
 int run_backward(const WindowAttnParams& p, cudaStream_t s) {
-    const int64_t rows = int64_t(p.B) * p.hq * p.Tp;
-    if (launch(window_delta_kernel<T>, p, dim3(unsigned((rows + 15) / 16)), 256, 0, s) != cudaSuccess) return DUO_ERR_CUDA;
+    const unsigned rows = unsigned(p.B) * p.hq * (p.Tp / (16 * kDeltaRows));
+    if (launch(window_delta_kernel<T>, p, dim3(rows), 256, 0, s) != cudaSuccess) return DUO_ERR_CUDA;
     const unsigned items = unsigned(p.items_kv + p.n_t * p.B * p.hq);
-    if (launch(window_bwd_kernel<T>, p, dim3(items), kBwdThreads, kBwdSmem, s) != cudaSuccess) return DUO_ERR_CUDA;
+    if (launch(window_bwd_kernel<T>, p, dim3(items), kThreads, kSmem, s) != cudaSuccess) return DUO_ERR_CUDA;
     const unsigned joins = unsigned(((p.p_long > 1 ? p.n_long : 0) + (p.p_short > 1 ? p.n_t - p.n_long : 0)) * p.B * p.n_kv);
     if (joins > 0 && launch(window_join_kernel<T>, p, dim3(16 * joins), 256, 0, s) != cudaSuccess) return DUO_ERR_CUDA;
     return DUO_OK;
@@ -1078,7 +1197,8 @@ int duo_window_attn_stats_bytes(const duo_window_attn_desc* d, size_t* bytes) {
     const int rc = duo::check_desc(d);
     if (rc) return rc;
     if (!bytes) return DUO_ERR_INVALID_ARG;
-    *bytes = size_t(d->batch) * d->num_q_heads * duo::padded(d->tokens) * 4;
+    // a number and 128 bytes per row
+    *bytes = size_t(d->batch) * d->num_q_heads * duo::padded(d->tokens) * (4 + duo::kTile);
     return DUO_OK;
 }
 
@@ -1089,7 +1209,7 @@ int duo_window_attn_workspace_bytes(const duo_window_attn_desc* d, size_t* bytes
     int sms = 0;
     if (duo::device_sms(&sms)) return DUO_ERR_CUDA;
     duo::WindowAttnParams p{};
-    duo::fill_params(p, *d, nullptr);
+    duo::fill_params(p, *d, nullptr, nullptr);
     duo::plan_pieces(p, sms);
     *bytes = duo::align256(size_t(d->batch) * d->num_q_heads * p.Tp * 4) +
              size_t(duo::partial_slots(p)) * 2 * duo::kTile * duo::kTile * 4;
@@ -1108,12 +1228,11 @@ int duo_window_attn(const duo_window_attn_desc* d, const duo_heads* q, const duo
     int sms = 0;
     if (duo::device_sms(&sms)) return DUO_ERR_CUDA;
     duo::WindowAttnParams p{};
-    duo::fill_params(p, *d, status);
+    duo::fill_params(p, *d, stats, status);
     if (!duo::make_map(&p.tm_q, *q, *d, p.hq) || !duo::make_map(&p.tm_k, *k, *d, p.n_kv) ||
         !duo::make_map(&p.tm_v, *v, *d, p.n_kv))
         return DUO_ERR_CUDA;
     p.out = duo::head_tensor(*out);
-    p.stats = stats;
     return d->dtype == DUO_BF16 ? duo::run_forward<__nv_bfloat16>(p, stream) : duo::run_forward<__half>(p, stream);
 }
 
@@ -1138,7 +1257,7 @@ int duo_window_attn_grad(const duo_window_attn_desc* d, const duo_heads* q, cons
     int sms = 0;
     if (duo::device_sms(&sms)) return DUO_ERR_CUDA;
     duo::WindowAttnParams p{};
-    duo::fill_params(p, *d, status);
+    duo::fill_params(p, *d, const_cast<float*>(stats), status);
     duo::plan_pieces(p, sms);
     if (!duo::make_map(&p.tm_q, *q, *d, p.hq) || !duo::make_map(&p.tm_k, *k, *d, p.n_kv) ||
         !duo::make_map(&p.tm_v, *v, *d, p.n_kv) || !duo::make_map(&p.tm_do, *dout, *d, p.hq))
@@ -1148,7 +1267,6 @@ int duo_window_attn_grad(const duo_window_attn_desc* d, const duo_heads* q, cons
     p.dq = duo::head_tensor(*dq);
     p.dk = duo::head_tensor(*dk);
     p.dv = duo::head_tensor(*dv);
-    p.stats = const_cast<float*>(stats);
     p.delta = static_cast<float*>(workspace);
     p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) +
                                       duo::align256(size_t(p.B) * p.hq * p.Tp * 4));

@@ -16,7 +16,8 @@ struct WindowAttnParams {
     CUtensorMap tm_q, tm_k, tm_v, tm_do;
     HeadTensor out, dout, dq, dk, dv;
     float* stats;            // [B][hq][Tp]: minus each row's log2-sum-exp of the scaled scores, -inf for no row
-    float* delta;            // [B][hq][Tp]: dot of each output row with its gradient
+    uint8_t* low;            // [B][hq][Tp][128]: what the rounding of the output took away, e5m2
+    float* delta;            // [B][hq][Tp]: minus the dot of each output row with its gradient
     float* part;             // partial dK, dV of key tiles whose rows are shared out
     const int32_t* lengths;  // may be null
     int32_t* status;         // may be null

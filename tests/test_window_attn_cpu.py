@@ -111,7 +111,7 @@ def test_pointer_refusals_and_empty_calls():
     for kw in (dict(batch=0), dict(tokens=0)):      # nothing to do
         L.duo_window_attn(_desc(L, **kw), None, None, None, None, None, None, None)
         L.duo_window_attn_grad(_desc(L, **kw), *[None] * 5, None, *[None] * 4, 0, None, None)
-    assert L.duo_window_attn_stats_bytes(_desc(L)) == 2 * 4 * 128 * 4
+    assert L.duo_window_attn_stats_bytes(_desc(L)) == 2 * 4 * 128 * (4 + 128)
 
 
 def test_python_refusals():
