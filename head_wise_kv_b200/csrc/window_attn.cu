@@ -173,13 +173,12 @@ __device__ __forceinline__ void mma_dims(uint32_t d, uint32_t a, uint32_t b, uin
     }
 }
 
-// D (+)= A B: A in TMEM (16-bit pairs, K steps of 8 columns; the second half
-// of K starts at column `second`), B a tile with its 128 rows along K.
-__device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, int second, uint32_t b, uint32_t idesc, bool add) {
+// D (+)= A B: A in TMEM (16-bit pairs, K steps of 8 columns from column a),
+// B a tile with its 128 rows along K; K steps k0 .. k1 - 1.
+__device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, int k0, int k1, uint32_t b, uint32_t idesc, bool add) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-        umma_f16_ts(d, a + (k >> 2) * second + (k & 3) * 8, smem_desc(b + k * 2048, kSlab, 1024), idesc,
-                    (add || k > 0) ? 1u : 0u);
+    for (int k = k0; k < k1; ++k)
+        umma_f16_ts(d, a + k * 8, smem_desc(b + k * 2048, kSlab, 1024), idesc, (add || k > k0) ? 1u : 0u);
 }
 
 __device__ __forceinline__ int length_of(const WindowAttnParams& p, int b) {
@@ -229,13 +228,13 @@ __device__ __forceinline__ T* row_at(const HeadTensor& x, int b, int h, int t) {
 // may have.  The dynamic region starts at a multiple of 1024 bytes (there is
 // no static one before it); the kernels leave with a status bit if not.
 constexpr int kThreads = 320;                        // warps 0-7 elementwise, 8 TMA, 9 products
-constexpr uint32_t kStatsAt = 7 * kTileBytes;        // [3][128] row statistics, [2][128] minus D
+constexpr uint32_t kStatsAt = 7 * kTileBytes;        // [3][128] minus D, [2][128] row statistics
 constexpr uint32_t kBarsAt = kStatsAt + 5 * kTile * 4;
 constexpr int kRing3 = 3, kRing2 = 2;                // stages of the two rings of tiles
 
 struct Bars {
     uint64_t once, full3[kRing3], empty3[kRing3], full2[kRing2], empty2[kRing2];
-    uint64_t s_full[2], s_read, dp_full, dp_read, p_full[2], ds_full, trimmed, done[2];
+    uint64_t s_full[2], s_read, dp_full, dp_read, p_half[2], p_full[2], ds_full[2], done[2];
     uint32_t tmem;
     int abort_flag;
 };
@@ -248,8 +247,9 @@ __device__ __forceinline__ Bars& bars_of(unsigned char* raw) { return *reinterpr
 __device__ __forceinline__ void set_up(Bars& sh, int p_arrivals) {
     if (threadIdx.x == 0) {
         for (uint64_t* bar = &sh.once; bar < reinterpret_cast<uint64_t*>(&sh.tmem); ++bar) mbar_init(smem_addr(bar), 1);
-        for (uint64_t* bar : {&sh.s_read, &sh.dp_read, &sh.ds_full, &sh.trimmed}) mbar_init(smem_addr(bar), 8);
-        for (uint64_t* bar : {&sh.p_full[0], &sh.p_full[1]}) mbar_init(smem_addr(bar), p_arrivals);
+        for (uint64_t* bar : {&sh.s_read, &sh.dp_read, &sh.ds_full[0], &sh.ds_full[1]}) mbar_init(smem_addr(bar), 8);
+        for (uint64_t* bar : {&sh.p_half[0], &sh.p_half[1], &sh.p_full[0], &sh.p_full[1]})
+            mbar_init(smem_addr(bar), p_arrivals);
         sh.abort_flag = 0;
         fence_mbar_init();
     }
@@ -257,6 +257,10 @@ __device__ __forceinline__ void set_up(Bars& sh, int p_arrivals) {
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+}
+
+__device__ __forceinline__ void fetch_map(const CUtensorMap* map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
 
 __device__ __forceinline__ void tear_down(Bars& sh) {
@@ -273,6 +277,48 @@ template <int STAGES>
 __device__ __forceinline__ void drain(uint64_t* full, int issued, unsigned long long limit) {
     for (int k = 1; k <= STAGES && k <= issued; ++k)
         mbar_wait(smem_addr(&full[(issued - k) % STAGES]), ((issued - k) / STAGES) & 1, limit);
+}
+
+// A finished tile leaves through shared memory and one TMA store: a thread
+// owns a row, and rows written straight to global memory would be 32 separate
+// lines per instruction (5000 cycles for a CTA's two tiles against 1500).
+// put_row: 32 columns of a row in the layout of a 128-byte swizzled box.
+__device__ __forceinline__ void put_row(uint32_t tile, int r, int col, const uint4* v) {
+#pragma unroll
+    for (int z = 0; z < 4; ++z) {
+        const int c = col / 8 + z;              // 16-byte piece of the row
+        st_shared_v4(tile + (c >> 3) * kSlab + r * 128 + ((c & 7) ^ (r & 7)) * 16, v[z]);
+    }
+}
+
+__device__ __forceinline__ void store_tile(const CUtensorMap* map, uint32_t tile, int t, int h, int b) {
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+        asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::"l"(
+                         reinterpret_cast<uint64_t>(map)),
+                     "r"(x * 64), "r"(t), "r"(h), "r"(b), "r"(tile + x * kSlab)
+                     : "memory");
+}
+
+// Whether every thread of a named barrier says yes (a warp whose wait ran out
+// says no, and none of them goes on).
+__device__ __forceinline__ bool all_agree(int id, int threads, bool yes) {
+    uint32_t out;
+    asm volatile(
+        "{\n\t.reg .pred pi, po;\n\t"
+        "setp.ne.u32 pi, %1, 0;\n\t"
+        "bar.red.and.pred po, %2, %3, pi;\n\t"
+        "selp.u32 %0, 1, 0, po;\n\t}"
+        : "=r"(out)
+        : "r"(uint32_t(yes)), "r"(id), "r"(threads)
+        : "memory");
+    return out != 0;
+}
+
+// The stores that this thread issued have read shared memory.
+__device__ __forceinline__ void stores_read() {
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
 }
 
 // This thread's warp has reached a point: one arrival, predicated (a branch
@@ -338,6 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
         if (p.status && threadIdx.x == 0) set_status(p.status, DUO_STATUS_WAIT_TIMEOUT);
         return;
     }
+    if (warp == 8 && lane < 4) fetch_map(lane == 0 ? &p.tm_q : lane == 1 ? &p.tm_k : lane == 2 ? &p.tm_v : &p.tm_out);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     // the query tiles with most keys first
@@ -391,15 +438,21 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
             for (int j = -1; ok && j < tiles.n; ++j) {
                 const int kt = j < 0 ? -1 : tiles.at(j), next = j + 1 < tiles.n ? tiles.at(j + 1) : -1;
                 const uint32_t k = sK + (j + 1) % kRing3 * kTileBytes, v = sV + max(j, 0) % kRing2 * kTileBytes;
+                // the tiles' own waits come before those for the softmax, which is later
                 if (next >= 0) ok = wait.thread(smem_addr(&sh.full3[(j + 1) % kRing3]), ((j + 1) / kRing3) & 1);
                 if (ok && j >= 0) ok = wait.thread(smem_addr(&sh.full2[j % kRing2]), (j / kRing2) & 1);
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     if (ok && j >= 0 && tiles.visits(x, kt)) {
+                        // the first half of the keys while the second half's weights are worked out
+                        ok = wait.thread(smem_addr(&sh.p_half[x]), seen[x] & 1);
+                        if (!ok) break;
+                        tc_fence_after();
+                        mma_rows(tmem + 256 + x * 128, tmem + x * 128, 0, 4, v, kPV, seen[x] > 0);
                         ok = wait.thread(smem_addr(&sh.p_full[x]), seen[x] & 1);
                         if (!ok) break;
                         tc_fence_after();
-                        mma_rows(tmem + 256 + x * 128, tmem + x * 128, 32, v, kPV, seen[x] > 0);
+                        mma_rows(tmem + 256 + x * 128, tmem + x * 128, 4, 8, v, kPV, true);
                         if (tiles.last(x, kt)) umma_commit(smem_addr(&sh.done[x]));
                         ++seen[x];
                     }
@@ -478,15 +531,20 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
                     ph[c / 2] = Elem<T>::pack(e.x, e.y);
                 }
                 tmem_stn<16>(at + q * 16, ph);
+                if (q == 1) {
+                    if (kt * kTile + kTile > len && len < p.T) {
+                        // the sequence ends inside its last key tile (which one query tile visits)
+                        ok = wait.warp(smem_addr(&sh.full2[j % kRing2]), (j / kRing2) & 1);
+                        if (!ok) break;
+                        zero_rows(sV + j % kRing2 * kTileBytes, len - kt * kTile, quarter, 4);
+                    }
+                    tmem_wait_st();
+                    arrive_warp(&sh.p_half[x]);
+                }
             }
+            if (!ok) break;
             const float2 sum = fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3]));
             l = l * alpha + (sum.x + sum.y);
-            if (kt * kTile + kTile > len && len < p.T) {
-                // the sequence ends inside its last key tile (which one query tile visits)
-                ok = wait.warp(smem_addr(&sh.full2[j % kRing2]), (j / kRing2) & 1);
-                if (!ok) break;
-                zero_rows(sV + j % kRing2 * kTileBytes, len - kt * kTile, quarter, 4);
-            }
             tmem_wait_st();
             arrive_warp(&sh.p_full[x]);
             ++seen;
@@ -496,13 +554,13 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
                 for (int c = 0; c < kTile; c += 8)
                     *reinterpret_cast<uint4*>(row_at<T>(p.out, b, h, i) + c) = make_uint4(0, 0, 0, 0);
             if (i < p.Tp) p.stats[row0 + i] = -CUDART_INF_F;
-        } else if (ok && wait.warp(smem_addr(&sh.done[x]), 0)) {
+        } else if (all_agree(1 + x, 128, ok && wait.warp(smem_addr(&sh.done[x]), 0))) {
             tc_fence_after();
             const bool row = i < len;
             const float inv = row && l > 0.f ? 1.f / l : 0.f;
             p.stats[row0 + i] = row && l > 0.f ? -(m + __log2f(l)) : -CUDART_INF_F;
-            T* dst = row_at<T>(p.out, b, h, i);
-            uint8_t* low = p.low + (row0 + i) * kTile;
+            // through this tile's Q and a K stage: all products that read them are done
+            const uint32_t tile = sQ + x * kTileBytes, low = sK + (tiles.n + x) % kRing3 * kTileBytes;
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 uint32_t o[32], hi[16], lo[8];
@@ -519,16 +577,22 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
                         : "f"((y.y - w.y) * kLowScale), "f"((y.x - w.x) * kLowScale));
                     lo[z / 4] = z % 4 == 0 ? f8 : lo[z / 4] | uint32_t(f8) << 16;
                 }
-                if (i < p.T) {
-#pragma unroll
-                    for (int z = 0; z < 4; ++z)
-                        *reinterpret_cast<uint4*>(dst + c * 32 + z * 8) =
-                            make_uint4(hi[4 * z], hi[4 * z + 1], hi[4 * z + 2], hi[4 * z + 3]);
-#pragma unroll
-                    for (int z = 0; z < 2; ++z)
-                        *reinterpret_cast<uint4*>(low + c * 32 + z * 16) =
-                            make_uint4(lo[4 * z], lo[4 * z + 1], lo[4 * z + 2], lo[4 * z + 3]);
-                }
+                const uint4 v[4] = {make_uint4(hi[0], hi[1], hi[2], hi[3]), make_uint4(hi[4], hi[5], hi[6], hi[7]),
+                                    make_uint4(hi[8], hi[9], hi[10], hi[11]), make_uint4(hi[12], hi[13], hi[14], hi[15])};
+                put_row(tile, r, c * 32, v);
+                st_shared_v4(low + r * 128 + c * 32, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+                st_shared_v4(low + r * 128 + c * 32 + 16, make_uint4(lo[4], lo[5], lo[6], lo[7]));
+            }
+            fence_proxy_async_smem();
+            named_bar_sync(1 + x, 128);
+            if ((warp & 3) == 0 && lane == 0) {
+                store_tile(&p.tm_out, tile, qt * kTile, h, b);
+                // rows behind the tensor's last one are this launch's own padding
+                asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
+                                 p.low + (row0 + qt * kTile) * kTile),
+                             "r"(low), "r"(uint32_t(kTile * kTile))
+                             : "memory");
+                stores_read();
             }
         }
     }
@@ -632,15 +696,11 @@ __device__ __forceinline__ void key_tile(const WindowAttnParams& p, Bars& sh, ui
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const KeyItem it(p, int(blockIdx.x));
     const uint32_t sK = smem, sV = sK + kTileBytes, sQ = sV + kTileBytes, sG = sQ + kRing3 * kTileBytes;
-    const uint32_t sStat = smem + kStatsAt, sDelta = sStat + kRing3 * kTile * 4;
+    // D comes with Q and goes with it after dK, the statistics with g and after dV:
+    // this step's D is read while its dV runs
+    const uint32_t sDelta = smem + kStatsAt, sStat = sDelta + kRing3 * kTile * 4;
     const int len = length_of(p, it.b), k0 = it.kt * kTile, n = it.x1 - it.x0;
     const uint32_t tmem = sh.tmem;
-    // whether the sequence ends inside query tile x of the list: its Q and g
-    // are zeroed behind the end before any product reads them
-    const auto cut = [&](int x) {
-        const int i0 = (it.kt + (it.x0 + x) % it.nq) * kTile;
-        return i0 + kTile > len && len < p.T;
-    };
 
     if (warp == 8) {
         if (lane == 0 && n > 0) {
@@ -656,13 +716,13 @@ __device__ __forceinline__ void key_tile(const WindowAttnParams& p, Bars& sh, ui
                 if (!wait.thread(smem_addr(&sh.empty3[q3]), ((x / kRing3) & 1) ^ 1)) break;
                 mbar_arrive_expect_tx(bar, kTileBytes + kTile * 4);
                 tma_tile(sQ + q3 * kTileBytes, &p.tm_q, i0, h, it.b, bar);
-                bulk_row(sStat + q3 * kTile * 4, p.stats + row, bar);
+                bulk_row(sDelta + q3 * kTile * 4, p.delta + row, bar);
                 ++qs;
                 bar = smem_addr(&sh.full2[g2]);
                 if (!wait.thread(smem_addr(&sh.empty2[g2]), ((x / kRing2) & 1) ^ 1)) break;
                 mbar_arrive_expect_tx(bar, kTileBytes + kTile * 4);
                 tma_tile(sG + g2 * kTileBytes, &p.tm_do, i0, h, it.b, bar);
-                bulk_row(sDelta + g2 * kTile * 4, p.delta + row, bar);
+                bulk_row(sStat + g2 * kTile * 4, p.stats + row, bar);
                 ++gs;
             }
             mbar_wait(smem_addr(&sh.once), 0, p.timeout_ns);
@@ -670,44 +730,39 @@ __device__ __forceinline__ void key_tile(const WindowAttnParams& p, Bars& sh, ui
             drain<kRing2>(sh.full2, gs, p.timeout_ns);
         }
     } else if (warp == 9) {
-        if (lane == 0) {
-            bool ok = n > 0 && wait.thread(smem_addr(&sh.once), 0);
-            int trims = 0;
-            const auto scores = [&](int x) {
-                if (!wait.thread(smem_addr(&sh.full3[x % kRing3]), (x / kRing3) & 1)) return false;
-                if (cut(x) && !wait.thread(smem_addr(&sh.trimmed), trims++ & 1)) return false;
-                mma_dims(tmem + kA, sK, sQ + x % kRing3 * kTileBytes, kDims);
+        if (lane == 0 && n > 0) {
+            // the tiles' own waits come before those for the elementwise warps, which are later
+            bool ok = wait.thread(smem_addr(&sh.once), 0);
+            for (int x = 0; ok && x <= n; ++x) {
+                const int q3 = x % kRing3, g2 = x % kRing2, last = x - 1;
+                if (x < n) ok = wait.thread(smem_addr(&sh.full3[q3]), (x / kRing3) & 1);
+                ok = ok && wait.thread(smem_addr(&sh.dp_read), x & 1);      // dP_{x-1} is in registers
+                if (!ok) break;
+                tc_fence_after();
+                if (x < n) mma_dims(tmem + kA, sK, sQ + q3 * kTileBytes, kDims);
                 umma_commit(smem_addr(&sh.s_full[0]));
-                return true;
-            };
-            const auto keys_grad = [&](int x) {
-                if (!wait.thread(smem_addr(&sh.ds_full), x & 1)) return false;
-                tc_fence_after();
-                mma_rows(tmem + kDK, tmem + kDS, 32, sQ + x % kRing3 * kTileBytes, kRows, x > 0);
-                umma_commit(smem_addr(&sh.empty3[x % kRing3]));
-                return true;
-            };
-            ok = ok && scores(0);
-            for (int x = 0; ok && x < n; ++x) {
-                const uint32_t tile = sG + x % kRing2 * kTileBytes;
-                ok = wait.thread(smem_addr(&sh.full2[x % kRing2]), (x / kRing2) & 1) &&
-                     wait.thread(smem_addr(&sh.s_read), x & 1);
+                if (x > 0) {
+                    ok = wait.thread(smem_addr(&sh.p_full[0]), last & 1);   // P_{x-1} is in its place
+                    if (!ok) break;
+                    tc_fence_after();
+                    mma_rows(tmem + kDV, tmem + kP, 0, 8, sG + (g2 ^ 1) * kTileBytes, kRows, x > 1);
+                    umma_commit(smem_addr(&sh.empty2[g2 ^ 1]));
+                }
+                if (x < n) ok = wait.thread(smem_addr(&sh.full2[g2]), (x / kRing2) & 1);
+                ok = ok && wait.thread(smem_addr(&sh.s_read), x & 1);       // S_x is in registers, dS_{x-1} in its place
                 if (!ok) break;
                 tc_fence_after();
-                mma_dims(tmem + kA, sV, tile, kDims);
-                umma_commit(smem_addr(&sh.dp_full));
-                if (x > 0) ok = keys_grad(x - 1);
-                ok = ok && wait.thread(smem_addr(&sh.dp_read), x & 1);
-                if (!ok) break;
-                tc_fence_after();
-                if (x + 1 < n) ok = scores(x + 1);
-                ok = ok && wait.thread(smem_addr(&sh.p_full[0]), x & 1);
-                if (!ok) break;
-                tc_fence_after();
-                mma_rows(tmem + kDV, tmem + kP, 32, tile, kRows, x > 0);
-                umma_commit(smem_addr(&sh.empty2[x % kRing2]));
+                if (x < n) {
+                    mma_dims(tmem + kA, sV, sG + g2 * kTileBytes, kDims);
+                    umma_commit(smem_addr(&sh.dp_full));
+                }
+                if (x > 0) {
+                    mma_rows(tmem + kDK, tmem + kDS, 0, 8, sQ + last % kRing3 * kTileBytes, kRows, x > 1);
+                    umma_commit(smem_addr(&sh.empty3[last % kRing3]));
+                }
             }
-            if (ok && n > 0) keys_grad(n - 1);
+        }
+        if (lane == 0) {
             umma_commit(smem_addr(&sh.done[0]));
             mbar_wait(smem_addr(&sh.done[0]), 0, p.timeout_ns);
         }
@@ -716,28 +771,41 @@ __device__ __forceinline__ void key_tile(const WindowAttnParams& p, Bars& sh, ui
         const int quarter = warp & 3, half = warp >> 2, r = quarter * 32 + lane, key = k0 + r, cb = half * 64;
         const uint32_t at = tmem + (uint32_t(quarter * 32) << 16);
         const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
+        // where the sequence ends inside query tile x of the list, what lies behind
+        // becomes zeros before any product
+        const auto trim = [&](uint64_t* full, uint32_t tile, int x, int phase) {
+            const int i0 = (it.kt + (it.x0 + x) % it.nq) * kTile;
+            if (!wait.warp(smem_addr(full), phase & 1)) return false;
+            zero_rows(tile, len - i0, warp, 8);
+            return true;
+        };
+        const int end_tile = len < p.T ? len / kTile : -1;     // the one that is cut (or none)
         bool ok = true;
-        for (int x = 0; x < n; ++x) {
-            const int qt = it.kt + (it.x0 + x) % it.nq, i0 = qt * kTile;
-            const uint32_t stat = sStat + x % kRing3 * kTile * 4 + cb * 4, delta = sDelta + x % kRing2 * kTile * 4 + cb * 4;
-            // the statistics came with Q, D with g: this warp's own waits for them
-            ok = wait.warp(smem_addr(&sh.full3[x % kRing3]), (x / kRing3) & 1);
+        uint32_t ph[32];               // P of a step, then its dS: stored once S of the next step is there
+        int qt = it.kt + (n > 0 ? it.x0 % it.nq : 0);
+        if (n > 0) {
+            if (qt == end_tile) ok = trim(&sh.full3[0], sQ, 0, 0);
+            if (ok) arrive_warp(&sh.dp_read);
+        }
+        for (int x = 0; ok && x < n; ++x) {
+            const int i0 = qt * kTile;
+            const uint32_t stat = sStat + x % kRing2 * kTile * 4 + cb * 4, delta = sDelta + x % kRing3 * kTile * 4 + cb * 4;
+            // this warp's own waits for the statistics and D, while S_x is worked out
+            ok = wait.warp(smem_addr(&sh.full2[x % kRing2]), (x / kRing2) & 1) &&
+                 wait.warp(smem_addr(&sh.full3[x % kRing3]), (x / kRing3) & 1);
             if (!ok) break;
-            if (cut(x)) {
-                ok = wait.warp(smem_addr(&sh.full2[x % kRing2]), (x / kRing2) & 1);
-                if (!ok) break;
-                zero_rows(sQ + x % kRing3 * kTileBytes, len - i0, warp, 8);
-                zero_rows(sG + x % kRing2 * kTileBytes, len - i0, warp, 8);
-                arrive_warp(&sh.trimmed);
-            }
+            if (qt == end_tile) zero_rows(sG + x % kRing2 * kTileBytes, len - i0, warp, 8);
+            // S_x: the products before it are done, dK_{x-2} among them
             ok = wait.warp(smem_addr(&sh.s_full[0]), x & 1);
             if (!ok) break;
             tc_fence_after();
+            if (x > 0) tmem_stn<32>(at + kDS + half * 32, ph);
             float s[64];
             uint32_t* u = reinterpret_cast<uint32_t*>(s);
             tmem_ld32p(at + kA + cb, u);
             tmem_ld32p(at + kA + cb + 32, u + 32);
             tmem_wait_ld();
+            tmem_wait_st();
             arrive_warp(&sh.s_read);
             if (qt == it.kt || !whole(p, qt, it.kt) || i0 + kTile > len) {
                 // rows i0 + c with key <= row < len, within the window unless the key is a sink
@@ -751,7 +819,6 @@ __device__ __forceinline__ void key_tile(const WindowAttnParams& p, Bars& sh, ui
                     for (int c = 0; c < 32; ++c) s[q * 32 + c] = (keep >> c) & 1u ? s[q * 32 + c] : -CUDART_INF_F;
                 }
             }
-            uint32_t ph[32];
 #pragma unroll
             for (int c = 0; c < 64; c += 4) {
                 const uint4 nl = lds128(stat + c * 4);
@@ -767,21 +834,22 @@ __device__ __forceinline__ void key_tile(const WindowAttnParams& p, Bars& sh, ui
                 ph[c / 2] = Elem<T>::pack(e[0], e[1]);
                 ph[c / 2 + 1] = Elem<T>::pack(e[2], e[3]);
             }
-            // P_{x-1} has been used
-            if (x > 0) ok = wait.warp(smem_addr(&sh.empty2[(x - 1) % kRing2]), ((x - 1) / kRing2) & 1);
-            if (!ok) break;
-            tc_fence_after();
-            tmem_stn<32>(at + kP + half * 32, ph);
-            tmem_wait_st();
-            arrive_warp(&sh.p_full[0]);
-            ok = wait.warp(smem_addr(&sh.full2[x % kRing2]), (x / kRing2) & 1) && wait.warp(smem_addr(&sh.dp_full), x & 1);
+            // dP_x: the products before it are done, dV_{x-1} among them
+            ok = wait.warp(smem_addr(&sh.dp_full), x & 1);
             if (!ok) break;
             tc_fence_after();
             uint32_t d[64];
             tmem_ld32p(at + kA + cb, d);
             tmem_ld32p(at + kA + cb + 32, d + 32);
+            if (++qt == it.kt + it.nq) qt = it.kt;
+            if (x + 1 < n && qt == end_tile)
+                ok = trim(&sh.full3[(x + 1) % kRing3], sQ + (x + 1) % kRing3 * kTileBytes, x + 1, (x + 1) / kRing3);
+            if (!ok) break;
             tmem_wait_ld();
             arrive_warp(&sh.dp_read);
+            tmem_stn<32>(at + kP + half * 32, ph);
+            tmem_wait_st();
+            arrive_warp(&sh.p_full[0]);
 #pragma unroll
             for (int c = 0; c < 64; c += 4) {
                 const uint4 dl = lds128(delta + c * 4);
@@ -795,18 +863,21 @@ __device__ __forceinline__ void key_tile(const WindowAttnParams& p, Bars& sh, ui
                 ph[c / 2] = Elem<T>::pack(y.x, y.y);
                 ph[c / 2 + 1] = Elem<T>::pack(z.x, z.y);
             }
-            // dS_{x-1} has been used
-            if (x > 0) ok = wait.warp(smem_addr(&sh.empty3[(x - 1) % kRing3]), ((x - 1) / kRing3) & 1);
-            if (!ok) break;
-            tc_fence_after();
-            tmem_stn<32>(at + kDS + half * 32, ph);
-            tmem_wait_st();
-            arrive_warp(&sh.ds_full);
         }
-        if (ok) ok = wait.warp(smem_addr(&sh.done[0]), 0);
-        if (ok) {
+        if (ok && n > 0) {             // dS of the last step, after dK of the one before
+            ok = wait.warp(smem_addr(&sh.s_full[0]), n & 1);
+            if (ok) {
+                tc_fence_after();
+                tmem_stn<32>(at + kDS + half * 32, ph);
+                tmem_wait_st();
+                arrive_warp(&sh.s_read);
+            }
+        }
+        if (all_agree(1, 256, ok && wait.warp(smem_addr(&sh.done[0]), 0))) {
             tc_fence_after();
             const bool row = key < len && n > 0;
+            // through the ring: all products that read it are done
+            const uint32_t tile[2] = {sQ, sQ + kTileBytes};
 #pragma unroll
             for (int w = 0; w < 2; ++w)
 #pragma unroll
@@ -814,21 +885,31 @@ __device__ __forceinline__ void key_tile(const WindowAttnParams& p, Bars& sh, ui
                     uint32_t o[32];
                     tmem_ld32(at + (w ? kDV : kDK) + cb + c * 32, o);
                     tmem_wait_ld();
-                    if (it.pieces > 1) {
-                        float4* y = reinterpret_cast<float4*>(p.part + it.slot * (2 * kTile * kTile) + w * kTile * kTile +
-                                                              r * kTile + cb + c * 32);
+                    if (it.pieces > 1) {        // four columns of 128 rows together: whole lines
+                        float4* y = reinterpret_cast<float4*>(p.part + it.slot * (2 * kTile * kTile) + w * kTile * kTile) +
+                                    (cb + c * 32) / 4 * kTile + r;
 #pragma unroll
                         for (int z = 0; z < 32; z += 4)
-                            y[z / 4] = row ? make_float4(__uint_as_float(o[z]), __uint_as_float(o[z + 1]),
-                                                         __uint_as_float(o[z + 2]), __uint_as_float(o[z + 3]))
-                                           : make_float4(0.f, 0.f, 0.f, 0.f);
-                    } else if (key < p.T) {
-                        T* dst = row_at<T>(w ? p.dv : p.dk, it.b, it.g, key) + cb + c * 32;
+                            y[z / 4 * kTile] = row ? make_float4(__uint_as_float(o[z]), __uint_as_float(o[z + 1]),
+                                                                 __uint_as_float(o[z + 2]), __uint_as_float(o[z + 3]))
+                                                   : make_float4(0.f, 0.f, 0.f, 0.f);
+                    } else {
+                        uint4 v[4];
 #pragma unroll
-                        for (int z = 0; z < 32; z += 8)
-                            *reinterpret_cast<uint4*>(dst + z) = row ? pack8<T>(o + z, w ? 1.f : p.scale) : make_uint4(0, 0, 0, 0);
+                        for (int z = 0; z < 4; ++z)
+                            v[z] = row ? pack8<T>(o + 8 * z, w ? 1.f : p.scale) : make_uint4(0, 0, 0, 0);
+                        put_row(tile[w], r, cb + c * 32, v);
                     }
                 }
+            if (it.pieces == 1) {
+                fence_proxy_async_smem();
+                named_bar_sync(1, 256);
+                if (warp == 0 && lane == 0) {
+                    store_tile(&p.tm_dk, tile[0], k0, it.g, it.b);
+                    store_tile(&p.tm_dv, tile[1], k0, it.g, it.b);
+                    stores_read();
+                }
+            }
         }
     }
 }
@@ -875,35 +956,43 @@ __device__ __forceinline__ void query_tile(const WindowAttnParams& p, Bars& sh, 
             drain<kRing2>(sh.full2, vs, p.timeout_ns);
         }
     } else if (warp == 9) {
-        if (lane == 0) {
-            bool ok = n > 0 && wait.thread(smem_addr(&sh.once), 0);
-            const auto keys = [&](int j) {
-                if (!wait.thread(smem_addr(&sh.full3[j % kRing3]), (j / kRing3) & 1)) return false;
-                if (cut && j == n - 1 && !wait.thread(smem_addr(&sh.trimmed), 0)) return false;
+        if (lane == 0 && n > 0) {
+            const auto scores = [&](int j) {
                 mma_dims(tmem + kS + (j & 1) * 128, sQ, sK + j % kRing3 * kTileBytes, kDims);
                 umma_commit(smem_addr(&sh.s_full[j & 1]));
-                return true;
             };
-            const auto values = [&](int j) {
-                if (!wait.thread(smem_addr(&sh.full2[j % kRing2]), (j / kRing2) & 1)) return false;
+            const auto weights_grad = [&](int j) {
                 mma_dims(tmem + kDP, sG, sV + j % kRing2 * kTileBytes, kDims);
                 umma_commit(smem_addr(&sh.dp_full));
                 umma_commit(smem_addr(&sh.empty2[j % kRing2]));
-                return true;
             };
-            ok = ok && keys(0) && values(0);
-            for (int j = 0; ok && j < n; ++j) {
-                if (j + 1 < n) ok = keys(j + 1);
-                ok = ok && wait.thread(smem_addr(&sh.dp_read), j & 1);
+            const auto here = [&](uint64_t* full, int phase) { return wait.thread(smem_addr(full), phase & 1); };
+            // the tiles' own waits come before those for the elementwise warps, which are later
+            bool ok = wait.thread(smem_addr(&sh.once), 0) && here(&sh.full3[0], 0) && here(&sh.full2[0], 0);
+            for (int j = 0; ok && j <= n; ++j) {
+                if (j + 1 < n) ok = here(&sh.full3[(j + 1) % kRing3], (j + 1) / kRing3);
+                ok = ok && wait.thread(smem_addr(&sh.ds_full[j & 1]), (j >> 1) & 1);      // dS_{j-1} is in its place
                 if (!ok) break;
                 tc_fence_after();
-                if (j + 1 < n) ok = values(j + 1);
-                ok = ok && wait.thread(smem_addr(&sh.ds_full), j & 1);
-                if (!ok) break;
-                tc_fence_after();
-                mma_rows(tmem + kDQ, tmem + kS + (j & 1) * 128, 64, sK + j % kRing3 * kTileBytes, kRows, j > 0);
-                umma_commit(smem_addr(&sh.empty3[j % kRing3]));
+                if (j == 0) {
+                    scores(0);
+                    weights_grad(0);
+                } else {
+                    mma_rows(tmem + kDQ, tmem + kS + ((j - 1) & 1) * 128, 0, 4, sK + (j - 1) % kRing3 * kTileBytes, kRows, j > 1);
+                    mma_rows(tmem + kDQ, tmem + kS + ((j - 1) & 1) * 128 + 32, 4, 8, sK + (j - 1) % kRing3 * kTileBytes, kRows,
+                             true);
+                    umma_commit(smem_addr(&sh.empty3[(j - 1) % kRing3]));
+                }
+                if (j + 1 < n) {
+                    scores(j + 1);       // over dS_{j-1}, whose product has been issued
+                    ok = here(&sh.full2[(j + 1) % kRing2], (j + 1) / kRing2) && wait.thread(smem_addr(&sh.dp_read), j & 1);
+                    if (!ok) break;      // dP_j is in registers
+                    tc_fence_after();
+                    weights_grad(j + 1);
+                }
             }
+        }
+        if (lane == 0) {
             umma_commit(smem_addr(&sh.done[0]));
             mbar_wait(smem_addr(&sh.done[0]), 0, p.timeout_ns);
         }
@@ -914,19 +1003,22 @@ __device__ __forceinline__ void query_tile(const WindowAttnParams& p, Bars& sh, 
         const int64_t row = (int64_t(b) * p.hq + h) * p.Tp + i;
         const float nl = p.stats[row], dl = p.delta[row];
         const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nl2 = make_float2(nl, nl), dl2 = make_float2(dl, dl);
+        // where the sequence ends inside the last key tile, what lies behind becomes
+        // zeros before any product
+        const auto trim = [&](uint64_t* full, uint32_t tile, int phase) {
+            if (!wait.warp(smem_addr(full), phase & 1)) return false;
+            zero_rows(tile, len - i0, warp, 8);
+            return true;
+        };
         bool ok = true;
-        for (int j = 0; j < n; ++j) {
+        if (n > 0) {
+            if (cut && n == 1) ok = trim(&sh.full3[0], sK, 0) && trim(&sh.full2[0], sV, 0);
+            if (cut && n == 2) ok = trim(&sh.full3[1], sK + kTileBytes, 0);
+            if (ok) arrive_warp(&sh.ds_full[0]);
+        }
+        for (int j = 0; ok && j < n; ++j) {
             const int kt = tiles.at(j);
             const uint32_t sb = kS + (j & 1) * 128;
-            if (cut && j == n - 1) {
-                // the sequence ends inside its last key tile; j - 1's products have used the rings' phases before
-                ok = wait.warp(smem_addr(&sh.full3[j % kRing3]), (j / kRing3) & 1) &&
-                     wait.warp(smem_addr(&sh.full2[j % kRing2]), (j / kRing2) & 1);
-                if (!ok) break;
-                zero_rows(sK + j % kRing3 * kTileBytes, len - i0, warp, 8);
-                zero_rows(sV + j % kRing2 * kTileBytes, len - i0, warp, 8);
-                arrive_warp(&sh.trimmed);
-            }
             ok = wait.warp(smem_addr(&sh.s_full[j & 1]), (j >> 1) & 1);
             if (!ok) break;
             tc_fence_after();
@@ -955,6 +1047,8 @@ __device__ __forceinline__ void query_tile(const WindowAttnParams& p, Bars& sh, 
             uint32_t d[64], ph[32];
             tmem_ld32p(at + kDP, d);
             tmem_ld32p(at + kDP + 32, d + 32);
+            if (cut && j + 2 == n) ok = trim(&sh.full2[(j + 1) % kRing2], sV + (j + 1) % kRing2 * kTileBytes, (j + 1) / kRing2);
+            if (!ok) break;
             tmem_wait_ld();
             arrive_warp(&sh.dp_read);
 #pragma unroll
@@ -964,24 +1058,31 @@ __device__ __forceinline__ void query_tile(const WindowAttnParams& p, Bars& sh, 
                 ph[c / 2] = Elem<T>::pack(y.x, y.y);
             }
             tmem_stn<32>(at + sb, ph);     // over this thread's own columns of S
+            if (cut && j + 3 == n) ok = trim(&sh.full3[(j + 2) % kRing3], sK + (j + 2) % kRing3 * kTileBytes, (j + 2) / kRing3);
+            if (!ok) break;
             tmem_wait_st();
-            arrive_warp(&sh.ds_full);
+            // S_{j+1} and dP_{j+1} may be here already: these warps can be a step
+            // ahead of the thread that waits for this, so two barriers take turns
+            arrive_warp(&sh.ds_full[(j + 1) & 1]);
         }
-        if (ok) ok = wait.warp(smem_addr(&sh.done[0]), 0);
-        if (ok) {
+        if (all_agree(1, 256, ok && wait.warp(smem_addr(&sh.done[0]), 0))) {
             tc_fence_after();
+            // through the ring: all products that read it are done
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 uint32_t o[32];
+                uint4 v[4];
                 tmem_ld32(at + kDQ + c * 32, o);
                 tmem_wait_ld();
-                if (i < p.T) {
-                    T* dst = row_at<T>(p.dq, b, h, i) + cb + c * 32;
 #pragma unroll
-                    for (int z = 0; z < 32; z += 8)
-                        *reinterpret_cast<uint4*>(dst + z) =
-                            i < len ? pack8<T>(o + z, p.scale) : make_uint4(0, 0, 0, 0);
-                }
+                for (int z = 0; z < 4; ++z) v[z] = i < len ? pack8<T>(o + 8 * z, p.scale) : make_uint4(0, 0, 0, 0);
+                put_row(sK, r, cb + c * 32, v);
+            }
+            fence_proxy_async_smem();
+            named_bar_sync(1, 256);
+            if (warp == 0 && lane == 0) {
+                store_tile(&p.tm_dq, sK, i0, h, b);
+                stores_read();
             }
         }
     }
@@ -996,6 +1097,9 @@ __global__ void __launch_bounds__(kThreads, 1) window_bwd_kernel(const __grid_co
         if (p.status && threadIdx.x == 0) set_status(p.status, DUO_STATUS_WAIT_TIMEOUT);
         return;
     }
+    if (threadIdx.x < 7)
+        fetch_map(threadIdx.x < 4 ? (threadIdx.x < 2 ? (threadIdx.x ? &p.tm_k : &p.tm_q) : (threadIdx.x == 2 ? &p.tm_v : &p.tm_do))
+                                  : (threadIdx.x == 4 ? &p.tm_dq : threadIdx.x == 5 ? &p.tm_dk : &p.tm_dv));
     set_up(sh, 8);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
@@ -1008,7 +1112,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_bwd_kernel(const __grid_co
 }
 
 // dK, dV of the key tiles whose rows were shared out: the pieces' sums, in
-// order.  Bound by HBM.  Sixteen blocks per key tile: 16 rows each of dK
+// order.  Bound by HBM.  Sixteen blocks per key tile: 16 columns each of dK
 // (first 8), then of dV.
 template <typename T>
 __global__ void __launch_bounds__(256) window_join_kernel(const __grid_constant__ WindowAttnParams p) {
@@ -1020,15 +1124,17 @@ __global__ void __launch_bounds__(256) window_join_kernel(const __grid_constant_
     const bool lng = tile < n_first;
     const int y = lng ? tile : tile - n_first, pieces = lng ? p.p_long : p.p_short;
     const int kt = y / bk + (lng ? 0 : p.n_long), b = y % bk / p.n_kv, g = y % p.n_kv;
-    const int w = blockIdx.x / 8 % 2, r = blockIdx.x % 8 * 16 + threadIdx.x / 16, c = threadIdx.x % 16 * 8;
+    // a warp: 8 columns of 32 rows
+    const int w = blockIdx.x / 8 % 2, c = (blockIdx.x % 8 * 2 + threadIdx.x / 128) * 8, r = threadIdx.x % 128;
     const int key = kt * kTile + r;
     if (key >= p.T) return;
     const int64_t first = (lng || p.p_long == 1 ? 0 : int64_t(p.n_long) * p.p_long * bk) +
                           int64_t(y / bk) * pieces * bk + y % bk;
     uint32_t o[8] = {};
     for (int k = 0; k < pieces; ++k) {
-        const float* src = p.part + (first + int64_t(k) * bk) * (2 * kTile * kTile) + w * kTile * kTile + r * kTile + c;
-        const float4 u = reinterpret_cast<const float4*>(src)[0], v = reinterpret_cast<const float4*>(src)[1];
+        const float4* src = reinterpret_cast<const float4*>(p.part + (first + int64_t(k) * bk) * (2 * kTile * kTile) +
+                                                            w * kTile * kTile) + c / 4 * kTile + r;
+        const float4 u = src[0], v = src[kTile];
         const float f[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int z = 0; z < 8; ++z) o[z] = __float_as_uint(__uint_as_float(o[z]) + f[z]);
@@ -1230,7 +1336,7 @@ int duo_window_attn(const duo_window_attn_desc* d, const duo_heads* q, const duo
     duo::WindowAttnParams p{};
     duo::fill_params(p, *d, stats, status);
     if (!duo::make_map(&p.tm_q, *q, *d, p.hq) || !duo::make_map(&p.tm_k, *k, *d, p.n_kv) ||
-        !duo::make_map(&p.tm_v, *v, *d, p.n_kv))
+        !duo::make_map(&p.tm_v, *v, *d, p.n_kv) || !duo::make_map(&p.tm_out, *out, *d, p.hq))
         return DUO_ERR_CUDA;
     p.out = duo::head_tensor(*out);
     return d->dtype == DUO_BF16 ? duo::run_forward<__nv_bfloat16>(p, stream) : duo::run_forward<__half>(p, stream);
@@ -1260,11 +1366,12 @@ int duo_window_attn_grad(const duo_window_attn_desc* d, const duo_heads* q, cons
     duo::fill_params(p, *d, const_cast<float*>(stats), status);
     duo::plan_pieces(p, sms);
     if (!duo::make_map(&p.tm_q, *q, *d, p.hq) || !duo::make_map(&p.tm_k, *k, *d, p.n_kv) ||
-        !duo::make_map(&p.tm_v, *v, *d, p.n_kv) || !duo::make_map(&p.tm_do, *dout, *d, p.hq))
+        !duo::make_map(&p.tm_v, *v, *d, p.n_kv) || !duo::make_map(&p.tm_do, *dout, *d, p.hq) ||
+        !duo::make_map(&p.tm_dq, *dq, *d, p.hq) || !duo::make_map(&p.tm_dk, *dk, *d, p.n_kv) ||
+        !duo::make_map(&p.tm_dv, *dv, *d, p.n_kv))
         return DUO_ERR_CUDA;
     p.out = duo::head_tensor(*out);
     p.dout = duo::head_tensor(*dout);
-    p.dq = duo::head_tensor(*dq);
     p.dk = duo::head_tensor(*dk);
     p.dv = duo::head_tensor(*dv);
     p.delta = static_cast<float*>(workspace);

@@ -14,7 +14,8 @@ struct HeadTensor {          // [batch][heads][tokens][128] by strides in elemen
 
 struct WindowAttnParams {
     CUtensorMap tm_q, tm_k, tm_v, tm_do;
-    HeadTensor out, dout, dq, dk, dv;
+    CUtensorMap tm_out, tm_dq, tm_dk, tm_dv;   // of results: whole tiles are stored through them
+    HeadTensor out, dout, dk, dv;
     float* stats;            // [B][hq][Tp]: minus each row's log2-sum-exp of the scaled scores, -inf for no row
     uint8_t* low;            // [B][hq][Tp][128]: what the rounding of the output took away, e5m2
     float* delta;            // [B][hq][Tp]: minus the dot of each output row with its gradient
