@@ -227,14 +227,14 @@ __device__ __forceinline__ T* row_at(const HeadTensor& x, int b, int h, int t) {
 // Both kernels use seven tiles and a little more, of the 227 KB that a CTA
 // may have.  The dynamic region starts at a multiple of 1024 bytes (there is
 // no static one before it); the kernels leave with a status bit if not.
-constexpr int kThreads = 320;                        // warps 0-7 elementwise, 8 TMA, 9 products
+constexpr int kThreads = 352;                        // warps 0-7 elementwise, 8 TMA, 9 and 10 products
 constexpr uint32_t kStatsAt = 7 * kTileBytes;        // [3][128] minus D, [2][128] row statistics
 constexpr uint32_t kBarsAt = kStatsAt + 5 * kTile * 4;
 constexpr int kRing3 = 3, kRing2 = 2;                // stages of the two rings of tiles
 
 struct Bars {
     uint64_t once, full3[kRing3], empty3[kRing3], full2[kRing2], empty2[kRing2];
-    uint64_t s_full[2], s_read, dp_full, dp_read, p_half[2], p_full[2], ds_full[2], done[2];
+    uint64_t s_full[2], s_read, dp_full, dp_read, p_half[2], p_full[2], ds_full[2], trimmed, done[2], fin;
     uint32_t tmem;
     int abort_flag;
 };
@@ -244,12 +244,16 @@ static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
 __device__ __forceinline__ Bars& bars_of(unsigned char* raw) { return *reinterpret_cast<Bars*>(raw + kBarsAt); }
 
 // Barriers (one arrival each unless said) and TMEM, by every warp of the CTA.
-__device__ __forceinline__ void set_up(Bars& sh, int p_arrivals) {
+__device__ __forceinline__ void set_up(Bars& sh, int p_arrivals, int empty3_arrivals, int empty2_arrivals) {
     if (threadIdx.x == 0) {
-        for (uint64_t* bar = &sh.once; bar < reinterpret_cast<uint64_t*>(&sh.tmem); ++bar) mbar_init(smem_addr(bar), 1);
-        for (uint64_t* bar : {&sh.s_read, &sh.dp_read, &sh.ds_full[0], &sh.ds_full[1]}) mbar_init(smem_addr(bar), 8);
+        for (uint64_t* bar : {&sh.once, &sh.full3[0], &sh.full3[1], &sh.full3[2], &sh.full2[0], &sh.full2[1], &sh.s_full[0],
+                              &sh.s_full[1], &sh.dp_full, &sh.done[0], &sh.done[1], &sh.fin})
+            mbar_init(smem_addr(bar), 1);
+        for (uint64_t* bar : {&sh.s_read, &sh.dp_read, &sh.ds_full[0], &sh.ds_full[1], &sh.trimmed}) mbar_init(smem_addr(bar), 8);
         for (uint64_t* bar : {&sh.p_half[0], &sh.p_half[1], &sh.p_full[0], &sh.p_full[1]})
             mbar_init(smem_addr(bar), p_arrivals);
+        for (uint64_t& bar : sh.empty3) mbar_init(smem_addr(&bar), empty3_arrivals);
+        for (uint64_t& bar : sh.empty2) mbar_init(smem_addr(&bar), empty2_arrivals);
         sh.abort_flag = 0;
         fence_mbar_init();
     }
@@ -319,6 +323,15 @@ __device__ __forceinline__ bool all_agree(int id, int threads, bool yes) {
 __device__ __forceinline__ void stores_read() {
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
     asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+
+// The end of a product warp: all that it issued has completed.
+__device__ __forceinline__ void finish_products(uint64_t* bar, unsigned long long limit) {
+    if ((threadIdx.x & 31) == 0) {
+        umma_commit(smem_addr(bar));
+        mbar_wait(smem_addr(bar), 0, limit);
+    }
+    __syncwarp();
 }
 
 // This thread's warp has reached a point: one arrival, predicated (a branch
@@ -402,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
         return;
     }
     const PairTiles tiles(p, pair, len);
-    set_up(sh, 4);
+    set_up(sh, 4, 1, 1);
     const uint32_t tmem = sh.tmem;
     const Waiter wait{p.status, p.timeout_ns, &sh.abort_flag};
 
@@ -428,8 +441,10 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
             drain<kRing3>(sh.full3, ks, p.timeout_ns);
             drain<kRing2>(sh.full2, vs, p.timeout_ns);
         }
-    } else if (warp == 9) {
-        if (lane == 0) {
+    } else if (warp >= 9) {
+        // one thread issues for both tiles (a warp for each: 163 us instead of 153, the
+        // two tiles' products then take turns and each lasts twice as long)
+        if (warp == 9 && lane == 0) {
             bool ok = wait.thread(smem_addr(&sh.once), 0);
             int seen[2] = {0, 0};               // key tiles that a and b have been through
             // S of both tiles' next key tile and P V of this one, a before b; the
@@ -559,8 +574,9 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
             const bool row = i < len;
             const float inv = row && l > 0.f ? 1.f / l : 0.f;
             p.stats[row0 + i] = row && l > 0.f ? -(m + __log2f(l)) : -CUDART_INF_F;
-            // through this tile's Q and a K stage: all products that read them are done
-            const uint32_t tile = sQ + x * kTileBytes, low = sK + (tiles.n + x) % kRing3 * kTileBytes;
+            // through this tile's Q, which no product reads any more
+            const uint32_t tile = sQ + x * kTileBytes;
+            uint4* low = reinterpret_cast<uint4*>(p.low + (row0 + qt * kTile) * kTile) + r;
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 uint32_t o[32], hi[16], lo[8];
@@ -580,18 +596,14 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
                 const uint4 v[4] = {make_uint4(hi[0], hi[1], hi[2], hi[3]), make_uint4(hi[4], hi[5], hi[6], hi[7]),
                                     make_uint4(hi[8], hi[9], hi[10], hi[11]), make_uint4(hi[12], hi[13], hi[14], hi[15])};
                 put_row(tile, r, c * 32, v);
-                st_shared_v4(low + r * 128 + c * 32, make_uint4(lo[0], lo[1], lo[2], lo[3]));
-                st_shared_v4(low + r * 128 + c * 32 + 16, make_uint4(lo[4], lo[5], lo[6], lo[7]));
+                // the remainders lie 16 of 128 rows together: whole lines
+                low[c * 2 * kTile] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                low[(c * 2 + 1) * kTile] = make_uint4(lo[4], lo[5], lo[6], lo[7]);
             }
             fence_proxy_async_smem();
             named_bar_sync(1 + x, 128);
             if ((warp & 3) == 0 && lane == 0) {
                 store_tile(&p.tm_out, tile, qt * kTile, h, b);
-                // rows behind the tensor's last one are this launch's own padding
-                asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
-                                 p.low + (row0 + qt * kTile) * kTile),
-                             "r"(low), "r"(uint32_t(kTile * kTile))
-                             : "memory");
                 stores_read();
             }
         }
@@ -624,7 +636,8 @@ __global__ void __launch_bounds__(256) window_delta_kernel(const __grid_constant
         if (t < len) {
             x[k] = *reinterpret_cast<const uint4*>(row_at<const T>(p.out, b, h, t) + part * 8);
             y[k] = *reinterpret_cast<const uint4*>(row_at<const T>(p.dout, b, h, t) + part * 8);
-            lo[k] = *reinterpret_cast<const uint2*>(p.low + (int64_t(bh) * p.Tp + t) * kTile + part * 8);
+            lo[k] = *reinterpret_cast<const uint2*>(p.low + (int64_t(bh) * p.Tp + t / kTile * kTile) * kTile +
+                                                       (part / 2 * kTile + t % kTile) * 16 + part % 2 * 8);
         }
     }
 #pragma unroll
@@ -730,43 +743,51 @@ __device__ __forceinline__ void key_tile(const WindowAttnParams& p, Bars& sh, ui
             drain<kRing2>(sh.full2, gs, p.timeout_ns);
         }
     } else if (warp == 9) {
-        if (lane == 0 && n > 0) {
-            // the tiles' own waits come before those for the elementwise warps, which are later
-            bool ok = wait.thread(smem_addr(&sh.once), 0);
-            for (int x = 0; ok && x <= n; ++x) {
-                const int q3 = x % kRing3, g2 = x % kRing2, last = x - 1;
-                if (x < n) ok = wait.thread(smem_addr(&sh.full3[q3]), (x / kRing3) & 1);
-                ok = ok && wait.thread(smem_addr(&sh.dp_read), x & 1);      // dP_{x-1} is in registers
-                if (!ok) break;
-                tc_fence_after();
-                if (x < n) mma_dims(tmem + kA, sK, sQ + q3 * kTileBytes, kDims);
+        // S and dP; warps wait as a whole and lane 0 issues
+        bool ok = n > 0 && wait.warp(smem_addr(&sh.once), 0);
+        for (int x = 0; ok && x < n; ++x) {
+            const int q3 = x % kRing3, g2 = x % kRing2;
+            ok = wait.warp(smem_addr(&sh.full3[q3]), (x / kRing3) & 1) && wait.warp(smem_addr(&sh.dp_read), x & 1);
+            if (!ok) break;                                                 // dP_{x-1} is in registers
+            tc_fence_after();
+            if (lane == 0) {
+                mma_dims(tmem + kA, sK, sQ + q3 * kTileBytes, kDims);
                 umma_commit(smem_addr(&sh.s_full[0]));
-                if (x > 0) {
-                    ok = wait.thread(smem_addr(&sh.p_full[0]), last & 1);   // P_{x-1} is in its place
-                    if (!ok) break;
-                    tc_fence_after();
-                    mma_rows(tmem + kDV, tmem + kP, 0, 8, sG + (g2 ^ 1) * kTileBytes, kRows, x > 1);
-                    umma_commit(smem_addr(&sh.empty2[g2 ^ 1]));
-                }
-                if (x < n) ok = wait.thread(smem_addr(&sh.full2[g2]), (x / kRing2) & 1);
-                ok = ok && wait.thread(smem_addr(&sh.s_read), x & 1);       // S_x is in registers, dS_{x-1} in its place
-                if (!ok) break;
-                tc_fence_after();
-                if (x < n) {
-                    mma_dims(tmem + kA, sV, sG + g2 * kTileBytes, kDims);
-                    umma_commit(smem_addr(&sh.dp_full));
-                }
-                if (x > 0) {
-                    mma_rows(tmem + kDK, tmem + kDS, 0, 8, sQ + last % kRing3 * kTileBytes, kRows, x > 1);
-                    umma_commit(smem_addr(&sh.empty3[last % kRing3]));
-                }
             }
+            __syncwarp();
+            ok = wait.warp(smem_addr(&sh.full2[g2]), (x / kRing2) & 1) && wait.warp(smem_addr(&sh.s_read), x & 1);
+            if (!ok) break;                                                 // S_x is in registers
+            tc_fence_after();
+            if (lane == 0) {
+                mma_dims(tmem + kA, sV, sG + g2 * kTileBytes, kDims);
+                umma_commit(smem_addr(&sh.dp_full));
+                umma_commit(smem_addr(&sh.empty2[g2]));      // dV lets g go too: it may be the earlier of the two
+            }
+            __syncwarp();
         }
-        if (lane == 0) {
-            umma_commit(smem_addr(&sh.done[0]));
-            mbar_wait(smem_addr(&sh.done[0]), 0, p.timeout_ns);
+        finish_products(&sh.fin, p.timeout_ns);
+    } else if (warp == 10) {
+        // dV and dK: a warp of their own, so that neither pair waits for the other's operands
+        bool ok = n > 0;
+        for (int x = 0; ok && x < n; ++x) {
+            ok = wait.warp(smem_addr(&sh.p_full[0]), x & 1);
+            if (!ok) break;
+            tc_fence_after();
+            if (lane == 0) {
+                mma_rows(tmem + kDV, tmem + kP, 0, 8, sG + x % kRing2 * kTileBytes, kRows, x > 0);
+                umma_commit(smem_addr(&sh.empty2[x % kRing2]));
+            }
+            __syncwarp();
+            ok = wait.warp(smem_addr(&sh.ds_full[0]), x & 1);
+            if (!ok) break;
+            tc_fence_after();
+            if (lane == 0) {
+                mma_rows(tmem + kDK, tmem + kDS, 0, 8, sQ + x % kRing3 * kTileBytes, kRows, x > 0);
+                umma_commit(smem_addr(&sh.empty3[x % kRing3]));
+            }
+            __syncwarp();
         }
-        __syncwarp();
+        finish_products(&sh.done[0], p.timeout_ns);
     } else {
         const int quarter = warp & 3, half = warp >> 2, r = quarter * 32 + lane, key = k0 + r, cb = half * 64;
         const uint32_t at = tmem + (uint32_t(quarter * 32) << 16);
@@ -781,12 +802,21 @@ __device__ __forceinline__ void key_tile(const WindowAttnParams& p, Bars& sh, ui
         };
         const int end_tile = len < p.T ? len / kTile : -1;     // the one that is cut (or none)
         bool ok = true;
-        uint32_t ph[32];               // P of a step, then its dS: stored once S of the next step is there
+        uint32_t ph[32];               // P of a step, then its dS: stored while dP of the next step is worked out
         int qt = it.kt + (n > 0 ? it.x0 % it.nq : 0);
         if (n > 0) {
             if (qt == end_tile) ok = trim(&sh.full3[0], sQ, 0, 0);
             if (ok) arrive_warp(&sh.dp_read);
         }
+        // dS of step x, once that of the step before has been used
+        const auto put_ds = [&](int x) {
+            if (x > 0 && !wait.warp(smem_addr(&sh.empty3[(x - 1) % kRing3]), ((x - 1) / kRing3) & 1)) return false;
+            tc_fence_after();
+            tmem_stn<32>(at + kDS + half * 32, ph);
+            tmem_wait_st();
+            arrive_warp(&sh.ds_full[0]);
+            return true;
+        };
         for (int x = 0; ok && x < n; ++x) {
             const int i0 = qt * kTile;
             const uint32_t stat = sStat + x % kRing2 * kTile * 4 + cb * 4, delta = sDelta + x % kRing3 * kTile * 4 + cb * 4;
@@ -795,18 +825,19 @@ __device__ __forceinline__ void key_tile(const WindowAttnParams& p, Bars& sh, ui
                  wait.warp(smem_addr(&sh.full3[x % kRing3]), (x / kRing3) & 1);
             if (!ok) break;
             if (qt == end_tile) zero_rows(sG + x % kRing2 * kTileBytes, len - i0, warp, 8);
-            // S_x: the products before it are done, dK_{x-2} among them
             ok = wait.warp(smem_addr(&sh.s_full[0]), x & 1);
             if (!ok) break;
             tc_fence_after();
-            if (x > 0) tmem_stn<32>(at + kDS + half * 32, ph);
             float s[64];
             uint32_t* u = reinterpret_cast<uint32_t*>(s);
             tmem_ld32p(at + kA + cb, u);
             tmem_ld32p(at + kA + cb + 32, u + 32);
             tmem_wait_ld();
-            tmem_wait_st();
             arrive_warp(&sh.s_read);
+            if (x > 0 && !put_ds(x - 1)) {
+                ok = false;
+                break;
+            }
             if (qt == it.kt || !whole(p, qt, it.kt) || i0 + kTile > len) {
                 // rows i0 + c with key <= row < len, within the window unless the key is a sink
                 int hi = len - 1 - i0;
@@ -834,7 +865,13 @@ __device__ __forceinline__ void key_tile(const WindowAttnParams& p, Bars& sh, ui
                 ph[c / 2] = Elem<T>::pack(e[0], e[1]);
                 ph[c / 2 + 1] = Elem<T>::pack(e[2], e[3]);
             }
-            // dP_x: the products before it are done, dV_{x-1} among them
+            // P_{x-1} has been used (and g_{x-1})
+            if (x > 0) ok = wait.warp(smem_addr(&sh.empty2[(x - 1) % kRing2]), ((x - 1) / kRing2) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            tmem_stn<32>(at + kP + half * 32, ph);
+            tmem_wait_st();
+            arrive_warp(&sh.p_full[0]);
             ok = wait.warp(smem_addr(&sh.dp_full), x & 1);
             if (!ok) break;
             tc_fence_after();
@@ -847,9 +884,6 @@ __device__ __forceinline__ void key_tile(const WindowAttnParams& p, Bars& sh, ui
             if (!ok) break;
             tmem_wait_ld();
             arrive_warp(&sh.dp_read);
-            tmem_stn<32>(at + kP + half * 32, ph);
-            tmem_wait_st();
-            arrive_warp(&sh.p_full[0]);
 #pragma unroll
             for (int c = 0; c < 64; c += 4) {
                 const uint4 dl = lds128(delta + c * 4);
@@ -864,15 +898,7 @@ __device__ __forceinline__ void key_tile(const WindowAttnParams& p, Bars& sh, ui
                 ph[c / 2 + 1] = Elem<T>::pack(z.x, z.y);
             }
         }
-        if (ok && n > 0) {             // dS of the last step, after dK of the one before
-            ok = wait.warp(smem_addr(&sh.s_full[0]), n & 1);
-            if (ok) {
-                tc_fence_after();
-                tmem_stn<32>(at + kDS + half * 32, ph);
-                tmem_wait_st();
-                arrive_warp(&sh.s_read);
-            }
-        }
+        if (ok && n > 0) ok = put_ds(n - 1);
         if (all_agree(1, 256, ok && wait.warp(smem_addr(&sh.done[0]), 0))) {
             tc_fence_after();
             const bool row = key < len && n > 0;
@@ -956,47 +982,47 @@ __device__ __forceinline__ void query_tile(const WindowAttnParams& p, Bars& sh, 
             drain<kRing2>(sh.full2, vs, p.timeout_ns);
         }
     } else if (warp == 9) {
-        if (lane == 0 && n > 0) {
-            const auto scores = [&](int j) {
-                mma_dims(tmem + kS + (j & 1) * 128, sQ, sK + j % kRing3 * kTileBytes, kDims);
+        bool ok = n > 0 && wait.warp(smem_addr(&sh.once), 0);
+        for (int j = 0; ok && j < n; ++j) {
+            const int k3 = j % kRing3, v2 = j % kRing2;
+            ok = wait.warp(smem_addr(&sh.full3[k3]), (j / kRing3) & 1);
+            if (ok && cut && j == n - 1) ok = wait.warp(smem_addr(&sh.trimmed), 0);
+            // dS_{j-2}, which lies in this S, has been used
+            if (ok && j > 1) ok = wait.warp(smem_addr(&sh.empty3[(j - 2) % kRing3]), ((j - 2) / kRing3) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            if (lane == 0) {
+                mma_dims(tmem + kS + (j & 1) * 128, sQ, sK + k3 * kTileBytes, kDims);
                 umma_commit(smem_addr(&sh.s_full[j & 1]));
-            };
-            const auto weights_grad = [&](int j) {
-                mma_dims(tmem + kDP, sG, sV + j % kRing2 * kTileBytes, kDims);
-                umma_commit(smem_addr(&sh.dp_full));
-                umma_commit(smem_addr(&sh.empty2[j % kRing2]));
-            };
-            const auto here = [&](uint64_t* full, int phase) { return wait.thread(smem_addr(full), phase & 1); };
-            // the tiles' own waits come before those for the elementwise warps, which are later
-            bool ok = wait.thread(smem_addr(&sh.once), 0) && here(&sh.full3[0], 0) && here(&sh.full2[0], 0);
-            for (int j = 0; ok && j <= n; ++j) {
-                if (j + 1 < n) ok = here(&sh.full3[(j + 1) % kRing3], (j + 1) / kRing3);
-                ok = ok && wait.thread(smem_addr(&sh.ds_full[j & 1]), (j >> 1) & 1);      // dS_{j-1} is in its place
-                if (!ok) break;
-                tc_fence_after();
-                if (j == 0) {
-                    scores(0);
-                    weights_grad(0);
-                } else {
-                    mma_rows(tmem + kDQ, tmem + kS + ((j - 1) & 1) * 128, 0, 4, sK + (j - 1) % kRing3 * kTileBytes, kRows, j > 1);
-                    mma_rows(tmem + kDQ, tmem + kS + ((j - 1) & 1) * 128 + 32, 4, 8, sK + (j - 1) % kRing3 * kTileBytes, kRows,
-                             true);
-                    umma_commit(smem_addr(&sh.empty3[(j - 1) % kRing3]));
-                }
-                if (j + 1 < n) {
-                    scores(j + 1);       // over dS_{j-1}, whose product has been issued
-                    ok = here(&sh.full2[(j + 1) % kRing2], (j + 1) / kRing2) && wait.thread(smem_addr(&sh.dp_read), j & 1);
-                    if (!ok) break;      // dP_j is in registers
-                    tc_fence_after();
-                    weights_grad(j + 1);
-                }
             }
+            __syncwarp();
+            ok = wait.warp(smem_addr(&sh.full2[v2]), (j / kRing2) & 1);
+            if (ok && j > 0) ok = wait.warp(smem_addr(&sh.dp_read), (j - 1) & 1);       // dP_{j-1} is in registers
+            if (!ok) break;
+            tc_fence_after();
+            if (lane == 0) {
+                mma_dims(tmem + kDP, sG, sV + v2 * kTileBytes, kDims);
+                umma_commit(smem_addr(&sh.dp_full));
+                umma_commit(smem_addr(&sh.empty2[v2]));
+            }
+            __syncwarp();
         }
-        if (lane == 0) {
-            umma_commit(smem_addr(&sh.done[0]));
-            mbar_wait(smem_addr(&sh.done[0]), 0, p.timeout_ns);
+        finish_products(&sh.fin, p.timeout_ns);
+    } else if (warp == 10) {
+        bool ok = n > 0;
+        for (int j = 0; ok && j < n; ++j) {
+            ok = wait.warp(smem_addr(&sh.ds_full[j & 1]), (j >> 1) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            if (lane == 0) {
+                const uint32_t ds = tmem + kS + (j & 1) * 128, k = sK + j % kRing3 * kTileBytes;
+                mma_rows(tmem + kDQ, ds, 0, 4, k, kRows, j > 0);
+                mma_rows(tmem + kDQ, ds + 32, 4, 8, k, kRows, true);
+                umma_commit(smem_addr(&sh.empty3[j % kRing3]));
+            }
+            __syncwarp();
         }
-        __syncwarp();
+        finish_products(&sh.done[0], p.timeout_ns);
     } else {
         const int quarter = warp & 3, half = warp >> 2, r = quarter * 32 + lane, i = i0 + r, cb = half * 64;
         const uint32_t at = tmem + (uint32_t(quarter * 32) << 16) + cb;
@@ -1004,22 +1030,23 @@ __device__ __forceinline__ void query_tile(const WindowAttnParams& p, Bars& sh, 
         const float nl = p.stats[row], dl = p.delta[row];
         const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nl2 = make_float2(nl, nl), dl2 = make_float2(dl, dl);
         // where the sequence ends inside the last key tile, what lies behind becomes
-        // zeros before any product
-        const auto trim = [&](uint64_t* full, uint32_t tile, int phase) {
-            if (!wait.warp(smem_addr(full), phase & 1)) return false;
-            zero_rows(tile, len - i0, warp, 8);
+        // zeros before any product, a step ahead
+        const auto trim = [&](int j) {
+            if (!wait.warp(smem_addr(&sh.full3[j % kRing3]), (j / kRing3) & 1) ||
+                !wait.warp(smem_addr(&sh.full2[j % kRing2]), (j / kRing2) & 1))
+                return false;
+            zero_rows(sK + j % kRing3 * kTileBytes, len - i0, warp, 8);
+            zero_rows(sV + j % kRing2 * kTileBytes, len - i0, warp, 8);
+            arrive_warp(&sh.trimmed);
             return true;
         };
         bool ok = true;
-        if (n > 0) {
-            if (cut && n == 1) ok = trim(&sh.full3[0], sK, 0) && trim(&sh.full2[0], sV, 0);
-            if (cut && n == 2) ok = trim(&sh.full3[1], sK + kTileBytes, 0);
-            if (ok) arrive_warp(&sh.ds_full[0]);
-        }
+        if (cut && n == 1) ok = trim(0);
         for (int j = 0; ok && j < n; ++j) {
             const int kt = tiles.at(j);
             const uint32_t sb = kS + (j & 1) * 128;
-            ok = wait.warp(smem_addr(&sh.s_full[j & 1]), (j >> 1) & 1);
+            if (cut && j + 2 == n) ok = trim(j + 1);
+            ok = ok && wait.warp(smem_addr(&sh.s_full[j & 1]), (j >> 1) & 1);
             if (!ok) break;
             tc_fence_after();
             float s[64];
@@ -1047,8 +1074,6 @@ __device__ __forceinline__ void query_tile(const WindowAttnParams& p, Bars& sh, 
             uint32_t d[64], ph[32];
             tmem_ld32p(at + kDP, d);
             tmem_ld32p(at + kDP + 32, d + 32);
-            if (cut && j + 2 == n) ok = trim(&sh.full2[(j + 1) % kRing2], sV + (j + 1) % kRing2 * kTileBytes, (j + 1) / kRing2);
-            if (!ok) break;
             tmem_wait_ld();
             arrive_warp(&sh.dp_read);
 #pragma unroll
@@ -1058,12 +1083,10 @@ __device__ __forceinline__ void query_tile(const WindowAttnParams& p, Bars& sh, 
                 ph[c / 2] = Elem<T>::pack(y.x, y.y);
             }
             tmem_stn<32>(at + sb, ph);     // over this thread's own columns of S
-            if (cut && j + 3 == n) ok = trim(&sh.full3[(j + 2) % kRing3], sK + (j + 2) % kRing3 * kTileBytes, (j + 2) / kRing3);
-            if (!ok) break;
             tmem_wait_st();
             // S_{j+1} and dP_{j+1} may be here already: these warps can be a step
-            // ahead of the thread that waits for this, so two barriers take turns
-            arrive_warp(&sh.ds_full[(j + 1) & 1]);
+            // ahead of the one that waits for this, so two barriers take turns
+            arrive_warp(&sh.ds_full[j & 1]);
         }
         if (all_agree(1, 256, ok && wait.warp(smem_addr(&sh.done[0]), 0))) {
             tc_fence_after();
@@ -1100,7 +1123,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_bwd_kernel(const __grid_co
     if (threadIdx.x < 7)
         fetch_map(threadIdx.x < 4 ? (threadIdx.x < 2 ? (threadIdx.x ? &p.tm_k : &p.tm_q) : (threadIdx.x == 2 ? &p.tm_v : &p.tm_do))
                                   : (threadIdx.x == 4 ? &p.tm_dq : threadIdx.x == 5 ? &p.tm_dk : &p.tm_dv));
-    set_up(sh, 8);
+    set_up(sh, 8, 1, int(blockIdx.x) < p.items_kv ? 2 : 1);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     const Waiter wait{p.status, p.timeout_ns, &sh.abort_flag};

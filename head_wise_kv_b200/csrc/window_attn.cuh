@@ -17,7 +17,8 @@ struct WindowAttnParams {
     CUtensorMap tm_out, tm_dq, tm_dk, tm_dv;   // of results: whole tiles are stored through them
     HeadTensor out, dout, dk, dv;
     float* stats;            // [B][hq][Tp]: minus each row's log2-sum-exp of the scaled scores, -inf for no row
-    uint8_t* low;            // [B][hq][Tp][128]: what the rounding of the output took away, e5m2
+    uint8_t* low;            // [B][hq][Tp / 128][128 / 16][128][16]: what the rounding of the output took
+                             // away, e5m2, 16 columns of 128 rows together
     float* delta;            // [B][hq][Tp]: minus the dot of each output row with its gradient
     float* part;             // partial dK, dV of key tiles whose rows are shared out
     const int32_t* lengths;  // may be null
