@@ -6,9 +6,11 @@
 // attention's forward and backward).  Nothing is computed here: every step of
 // the path runs in the library's kernels (duo_kv.h).
 #include <ATen/core/grad_mode.h>
+#include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/functions/basic_ops.h>
+#include <torch/csrc/autograd/variable.h>
 #include <torch/extension.h>
 
 #include <limits>
@@ -59,6 +61,21 @@ void need(const Tensor& t, const char* name, at::ScalarType type, at::IntArrayRe
 const int32_t* ints(const Tensor& t) { return static_cast<const int32_t*>(t.data_ptr()); }
 const int32_t* ints(const OptTensor& t) { return t ? ints(*t) : nullptr; }
 
+// A backward pass captured into a graph must not meet a leaf whose gradient
+// node lives on another stream (an eager graph of the same leaf keeps it): the
+// engine would make the capture wait for a stream outside it, on a thread of
+// its own, where the error ends the process.  Refused here instead.
+void check_capture(const Tensor& t, const char* name) {
+    if (!t.requires_grad() || !t.is_leaf() || !at::GradMode::is_enabled()) return;
+    if (c10::cuda::currentStreamCaptureStatusMayInitCtx() == c10::cuda::CaptureStatus::None) return;
+    const auto node = torch::autograd::impl::try_get_grad_accumulator(t);
+    if (!node) return;
+    const auto stream = node->stream();
+    TORCH_CHECK_VALUE(!stream || *stream == c10::cuda::getCurrentCUDAStream(t.device().index()).unwrap(), name,
+                      " is a leaf of an eager graph that is still alive: drop that graph, or give the capture a leaf of its "
+                      "own, before its backward pass is captured");
+}
+
 cudaStream_t stream_of(const at::Device& dev) { return c10::cuda::getCurrentCUDAStream(dev.index()).stream(); }
 
 // ------------------------------------------------------------------ rotary positions
@@ -79,7 +96,8 @@ Tensor rope_apply(uintptr_t plan, int64_t d, const Tensor& x, const Tensor& posi
     TORCH_CHECK_VALUE(dev.is_cuda(), "the tensors must be on a CUDA device");
     TORCH_CHECK_VALUE(x.dim() == 4 && x.size(3) == d, "shape ", shape_of(x.sizes()), ", expected [batch][heads][tokens][", d,
                       "]");
-    const int64_t B = x.size(0), H = x.size(1), n = x.size(2);
+    const int64_t B = x.size(0), H = x.size(1), n = x.size(2), top = std::numeric_limits<int32_t>::max();
+    TORCH_CHECK_VALUE(B <= top && H <= top && n <= top, "too large a tensor");
     const bool per_token = positions.dim() == 2;
     TORCH_CHECK_VALUE(positions.scalar_type() == at::kInt && positions.device() == dev && positions.is_contiguous(),
                       "positions must be contiguous int32 on the tensors' device");
@@ -398,6 +416,7 @@ Tensor window_attention(const Tensor& q, const Tensor& k, const Tensor& v, int64
                          names[i], ": dtype ", t.scalar_type(), ", expected bfloat16 or float16, the same for q, k and v");
         TORCH_CHECK_VALUE(t.is_cuda() && t.device() == q.device(), names[i], ": on ", t.device(),
                           ", expected one CUDA device for q, k and v");
+        check_capture(t, names[i]);
         TORCH_CHECK_VALUE(t.dim() == 4, names[i], ": shape ", shape_of(t.sizes()), ", expected [batch][heads][tokens][128]");
     }
     const int64_t B = q.size(0), hq = q.size(1), T = q.size(2), d = q.size(3), n_kv = k.size(1);
@@ -439,6 +458,7 @@ PYBIND11_MODULE(TORCH_EXTENSION_NAME, m) {
         }
     });
     m.def("rope_apply", &rope_apply);
+    m.def("check_capture", [](const Tensor& t) { check_capture(t, "x"); });
     py::class_<Cache>(m, "Cache")
         .def(py::init<uintptr_t, int64_t, int64_t, int64_t, int64_t, int64_t>())
         .def("append_rope", &Cache::append_rope)

@@ -110,6 +110,7 @@ class Rope:
         if x.requires_grad and torch.is_grad_enabled():
             if out is not None:
                 raise ValueError("out cannot be given where a gradient is recorded")
+            _b.check_capture(x)
             return _RopeFunction.apply(x, positions, n_new, self, bool(transpose))
         return self._apply(x, positions, n_new, transpose, out)
 

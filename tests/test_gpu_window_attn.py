@@ -244,6 +244,31 @@ def test_same_bits_again_on_another_stream_and_in_a_graph():
         assert all(torch.equal(a, b) for a, b in zip(res, _run(*new, 64, 128)))
 
 
+def test_second_derivatives_and_foreign_captures_are_refused():
+    from head_wise_kv_b200 import Rope, window_attention
+    x = [t.detach().requires_grad_() for t in _make(1, 2, 1, 40, torch.bfloat16, False, 18)[:3]]
+    out = window_attention(*x, 2, 9)
+    gq, gk, gv = torch.autograd.grad(out.float().sum(), x, create_graph=True)
+    assert gq.requires_grad
+    with pytest.raises(RuntimeError, match="once"):
+        (gq.float() ** 2).sum().backward()
+    # the eager graph of these leaves lives: a capture with the same leaves is refused, one with its own is not
+    keep = window_attention(*x, 2, 9)
+    rope, pos = Rope(128), torch.zeros(1, dtype=torch.int32, device=DEV)
+    for call in (lambda: window_attention(*x, 2, 9), lambda: rope.apply(x[0], pos)):
+        graph = torch.cuda.CUDAGraph()
+        with pytest.raises(ValueError, match="eager graph"):
+            with torch.cuda.graph(graph):
+                call()
+    torch.cuda.synchronize()
+    y = [t.detach().requires_grad_() for t in x]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = torch.autograd.grad(window_attention(*y, 2, 9).float().sum(), y)
+    graph.replay()
+    assert all(torch.equal(a, b) for a, b in zip(got, torch.autograd.grad(keep.float().sum(), x)))
+
+
 def test_empty_and_refusals():
     from head_wise_kv_b200 import window_attention, window_attention_status
     q, k, v, g = _make(2, 4, 2, 20, torch.bfloat16, False, 17)
