@@ -15,8 +15,8 @@
 // in flight and four blocks per SM.  Keys and values of streaming heads that
 // the ring will not hold are not read.
 // Measured: 8 prompts of 8192 tokens, 32 query / 8 KV heads of 128, bf16:
-// 242 us for 1.34 GB (85% of the copy rate); 6205 ragged tokens into FP8
-// pages: 35 us for 122 MB, where address arithmetic, code conversion and the
+// 238 us for 1.34 GB (86% of the copy rate); 6205 ragged tokens into FP8
+// pages: 31 us for 122 MB, where address arithmetic, code conversion and the
 // map's dependent loads count.  Angles per thread and group of heads instead
 // of per block: 248 and 48 us; four heads in flight with three blocks per SM:
 // 244 and 36 us.

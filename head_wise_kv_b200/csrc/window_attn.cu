@@ -25,6 +25,11 @@
 // No atomics: the backward visits each tile pair twice, once for the key
 // tile's owner (dK, dV) and once for the query tile's (dQ).  That is 7
 // products per pair instead of 5, and every sum is taken in one fixed order.
+//
+// Measured, 32 query / 8 KV heads, 4096 tokens, bf16, every key: forward 153 us
+// (137 GFLOP, 900 TFLOP/s), backward 454 us (344 GFLOP in five products, 760
+// TFLOP/s; 1060 counting the seven that are done), at the board's power limit.
+// 16 / 4 heads, 8192 tokens, window 1024, 64 sinks: 118 and 294 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -360,6 +365,11 @@ __device__ __forceinline__ void arrive_warp(uint64_t* bar) {
 //     than 2^8), P_j, O / l at the end.
 // Beside the result each row leaves its statistics and what the rounding of
 // the result took away (in 8 bits), for D_i in the backward.
+// Bound by the chain scores - softmax - P V of each tile: a step of both tiles
+// has 2048 cycles of products and, at 16 a cycle, 2048 of exponentials; 153 us
+// over the steps of an SM is about twice that.  One query tile per CTA with
+// waits by whole warps measured 171 us, two tiles 169, and 153 with the weights
+// handed over in halves and results that leave through TMA.
 constexpr float kLowScale = 1024.f;      // of the rounding's remainder: 2^-26 .. 56 without loss of its leading bits
 
 // The key tiles of two neighbouring query tiles: those of the first and of
