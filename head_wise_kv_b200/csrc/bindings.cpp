@@ -5,6 +5,7 @@
 // ctypes cost more than that (8 to 15 us a call, 200 us for a small
 // attention's forward and backward).  Nothing is computed here: every step of
 // the path runs in the library's kernels (duo_kv.h).
+#include <ATen/MemoryOverlap.h>
 #include <ATen/core/grad_mode.h>
 #include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAGuard.h>
@@ -117,6 +118,11 @@ Tensor rope_apply(uintptr_t plan, int64_t d, const Tensor& x, const Tensor& posi
         out = n_new ? at::zeros(x.sizes(), x.options()) : at::empty(x.sizes(), x.options());
     }
     TORCH_CHECK_VALUE(x.stride(3) == 1 && out.stride(3) == 1, "the elements of a head must be contiguous");
+    if (given) {       // in place each thread writes what it has read; any other overlap would be a race
+        TORCH_CHECK_VALUE(at::has_internal_overlap(out) != at::MemOverlap::Yes, "out must not overlap itself");
+        TORCH_CHECK_VALUE(at::get_overlap_status(out, x) != at::MemOverlapStatus::Partial,
+                          "out must be x or lie apart from it");
+    }
     duo_rope_tensor t{};
     t.in = x.data_ptr();
     t.out = out.data_ptr();

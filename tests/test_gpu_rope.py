@@ -184,3 +184,19 @@ def test_refusals():
     rope.close()
     with pytest.raises(DuoError):
         rope.apply(x, pos)
+
+
+def test_out_that_overlaps_is_refused():
+    """out may be x or lie apart from it; a shifted or expanded one would be a race between rows."""
+    from head_wise_kv_b200 import Rope
+    r = Rope(64)
+    flat = torch.arange(3 * 64 * 4, device=DEV, dtype=torch.float32)
+    x, shifted = flat[:512].view(1, 2, 4, 64), flat[64:576].view(1, 2, 4, 64)
+    pos = torch.zeros(1, dtype=torch.int32, device=DEV)
+    keep = flat.clone()
+    for out in (shifted, flat[:64].expand(1, 2, 4, 64), x.transpose(1, 2).reshape(1, 4, 2, 64)[:, :2, :1].expand(1, 2, 4, 64)):
+        with pytest.raises(ValueError):
+            r.apply(x, pos, out=out)
+    assert torch.equal(flat, keep)
+    want = r.apply(x, pos)
+    assert r.apply(x, pos, out=x) is not None and torch.equal(x, want)
