@@ -292,7 +292,9 @@ struct Cache {
 };
 
 // ------------------------------------------------------------------ windowed attention
-// One status word per device, never freed: kernels may still hold it when the process ends.
+// One status word per device, never freed: kernels may still hold it when the process ends.  It is
+// memory of its own, cleared before the call goes on: made by the allocator in a captured call, its
+// clearing would belong to the graph, and each replay would take back the bits of other calls.
 Tensor status_word(const at::Device& dev) {
     static std::mutex lock;
     static auto* words = new std::vector<Tensor>();
@@ -301,7 +303,17 @@ Tensor status_word(const at::Device& dev) {
     if (words->size() <= i) words->resize(i + 1);
     if (!(*words)[i].defined()) {
         const c10::cuda::CUDAGuard guard(dev);
-        (*words)[i] = at::zeros({1}, at::TensorOptions().dtype(at::kInt).device(dev));
+        const c10::cuda::CUDAStreamCaptureModeGuard relaxed(cudaStreamCaptureModeRelaxed);
+        void* word = nullptr;
+        cudaStream_t own = nullptr;
+        C10_CUDA_CHECK(cudaStreamCreateWithFlags(&own, cudaStreamNonBlocking));
+        cudaError_t e = cudaMalloc(&word, sizeof(int32_t));
+        if (e == cudaSuccess) e = cudaMemsetAsync(word, 0, sizeof(int32_t), own);
+        if (e == cudaSuccess) e = cudaStreamSynchronize(own);
+        (void)cudaStreamDestroy(own);
+        if (e != cudaSuccess && word) (void)cudaFree(word);
+        C10_CUDA_CHECK(e);
+        (*words)[i] = at::from_blob(word, {1}, at::TensorOptions().dtype(at::kInt).device(dev));
     }
     return (*words)[i];
 }
@@ -472,4 +484,5 @@ PYBIND11_MODULE(TORCH_EXTENSION_NAME, m) {
         .def("step_rope", &Cache::step_rope);
     m.def("window_attention", &window_attention);
     m.def("window_attention_status", &window_attention_status);
+    m.def("status_word", [](int64_t device) { return status_word(at::Device(at::kCUDA, at::DeviceIndex(device))); });
 }

@@ -332,3 +332,42 @@ def test_gated_branches_with_rotary_positions():
     # the gate's gradient: 2 T B 128 terms |w| |branch| with errors of rms 2^-8 of the branches' size
     scale = float((w.double() ** 2 * (branch(0, 0).detach() ** 2 + branch(S, W).detach() ** 2)).sum((0, 2, 3)).sqrt().max())
     assert float((g_alpha.double() - r_alpha).abs().max()) <= 4 * 2.0 ** -8 * scale
+
+
+_FIRST_IN_CAPTURE = """
+import torch
+from head_wise_kv_b200 import window_attention, window_attention_status
+x = [torch.randn(1, 2, 40, 128, device="cuda:0", dtype=torch.bfloat16) for _ in range(3)]
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = window_attention(*x, 2, 9)
+assert window_attention_status("cuda:0") == 0
+from head_wise_kv_b200 import _binding
+word = _binding.status_word(0)
+word.fill_(64)
+graph.replay()
+assert window_attention_status("cuda:0") == 64
+assert torch.equal(got, window_attention(*x, 2, 9)) and window_attention_status("cuda:0") == 0
+"""
+
+
+def test_status_outlives_a_graph_captured_first():
+    """The first call of a process inside a capture: replays leave the status bits of other calls."""
+    import subprocess
+    import sys
+    done = subprocess.run([sys.executable, "-c", _FIRST_IN_CAPTURE], capture_output=True, text=True, timeout=240)
+    assert done.returncode == 0, done.stderr[-2000:]
+
+
+def test_a_dimension_of_one_entry_has_any_stride():
+    from head_wise_kv_b200 import window_attention
+    x = [torch.randn(1, 1, 50, 128, device=DEV, dtype=torch.bfloat16) for _ in range(3)]
+    want = window_attention(*x, 1, 7)
+    odd = [t.as_strided(t.shape, (3, 5, 128, 1)) for t in x]
+    assert torch.equal(window_attention(*odd, 1, 7), want)
+    g = torch.randn_like(want)
+    a, b = ([t.detach().requires_grad_() for t in y] for y in (x, odd))
+    ga = torch.autograd.grad(window_attention(*a, 1, 7), a, g)
+    gb = torch.autograd.grad(window_attention(*b, 1, 7), b, g)
+    assert all(torch.equal(s, t) for s, t in zip(ga, gb))
