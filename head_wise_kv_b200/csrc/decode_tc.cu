@@ -452,8 +452,9 @@ __global__ void __launch_bounds__(I4 ? kThreadsI4 : kThreads, 1)
     // be stale (the last row of a retrieval segment, one slot of a streaming
     // ring): the lengths, q and every other tile are read at once, and a
     // producer waits for the append before the first tile that may hold such
-    // a row, as the q warp does for queries that the append rotates (q_late).  Any sequence whose length does not grow by exactly one turns
-    // this off for the launch.
+    // a row, as the q warp does for queries that the append rotates (q_late).
+    // Any sequence whose length does not grow by exactly one turns this off for
+    // the launch.
     const bool step_mode = p.len_before != nullptr;
     if (!step_mode) asm volatile("griddepcontrol.wait;" ::: "memory");
     build_prefix<BLK>(p, bpre);
