@@ -313,8 +313,8 @@ class DuoKVCache:
         [T][n_kv][d] with T = tokens.max_tokens.  Without it: a padded batch
         [B][n][heads][d] and n_new int32 [B] (<= n).  len_before: int32 [B].
         q may be None (keys and values only).  Returns the rotated queries
-        (contiguous, in ``out`` if given; rows without a token stay as they
-        were, zero where out is new)."""
+        (contiguous, in ``out`` if given, which lies apart from q, k and v;
+        rows without a token stay as they were, zero where out is new)."""
         return self._calls.append_rope(layer, rope.handle or 0, rope.d, q, k, v, len_before, tokens, n_new, out)
 
     def step_rope(self, layer: int, rope, q, k, v, len_before, lengths, scale: float, out=None, lse=None,

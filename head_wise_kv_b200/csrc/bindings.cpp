@@ -214,6 +214,11 @@ struct Cache {
             shape.push_back(d);
             if (given) {
                 need(*given, "out", at::kBFloat16, shape, dev);
+                for (const Tensor& in : {*q, k, v}) {
+                    const auto lap = at::get_overlap_status(*given, in);
+                    TORCH_CHECK_VALUE(lap != at::MemOverlapStatus::Partial && lap != at::MemOverlapStatus::Full,
+                                      "out must lie apart from q, k and v");
+                }
                 out = given;
             } else {        // rows without a token are zero where out is new
                 out = ragged || n_new ? at::zeros(shape, k.options()) : at::empty(shape, k.options());

@@ -572,8 +572,8 @@ typedef struct {
  *     b * n_tokens + i holds token i of sequence b, at position
  *     len_before[b] + i; n_new: device int32 [batch] (<= n_tokens) or NULL =
  *     n_tokens for every sequence;
- *   q_out: [rows][num_q_heads][d] bf16, contiguous; rows without a token stay
- *     as they were.
+ *   q_out: [rows][num_q_heads][d] bf16, contiguous, apart from q, k and v;
+ *     rows without a token stay as they were.
  * rope's head_dim is the cache's.  The cache's device must be the current
  * one (else INVALID_ARG).  A map entry out of range is skipped and sets
  * DUO_STATUS_BAD_LENGTH (sequence, position), OVER_CAPACITY or NO_PAGE. */

@@ -383,3 +383,16 @@ def test_captured_steps():
         assert torch.equal(out, ref) and torch.equal(tokens.len_after, after)
     assert st.caches[0].status() == st.caches[1].status() == 0
     assert torch.equal(st.caches[0].page_state()["table"], st.caches[1].page_state()["table"])
+
+
+def test_rotated_queries_over_an_input_are_refused():
+    st = Setup("bf16", B=2)
+    c = st.caches[0]
+    x = torch.zeros(2, 1, 8, 128, dtype=torch.bfloat16, device=DEV)
+    k, v = (torch.zeros(2, 1, 4, 128, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    pool = torch.zeros(2 * 12 * 128, dtype=torch.bfloat16, device=DEV)
+    inside, over = pool[:1024].view(2, 1, 4, 128), pool[:2048].view(2, 1, 8, 128)
+    zero = torch.zeros(2, dtype=torch.int32, device=DEV)
+    for args in ((x, k, v, x), (x, inside, v, over), (x, k, inside, over)):
+        with pytest.raises(ValueError):
+            c.append_rope(0, st.rope, *args[:3], zero, out=args[3])
