@@ -29,7 +29,7 @@
 // Measured, 32 query / 8 KV heads, 4096 tokens, bf16, every key: forward 153 us
 // (137 GFLOP, 900 TFLOP/s), backward 454 us (344 GFLOP in five products, 760
 // TFLOP/s; 1060 counting the seven that are done), at the board's power limit.
-// 16 / 4 heads, 8192 tokens, window 1024, 64 sinks: 118 and 294 us.
+// 16 / 4 heads, 8192 tokens, window 1024, 64 sinks: 113 and 294 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -376,11 +376,9 @@ constexpr float kLowScale = 1024.f;      // of the rounding's remainder: 2^-26 .
 // the second one in one list.
 struct PairTiles {
     int qa, lo_b, sink_tiles, sinks, lo, hi, n;
-    bool full;
-    __device__ __forceinline__ PairTiles(const WindowAttnParams& p, int pair, int len) {
-        qa = 2 * pair;
-        full = p.full;
-        hi = (qa + 1) * kTile < len ? qa + 1 : qa;
+    __device__ __forceinline__ PairTiles(const WindowAttnParams& p, int first, int count, int len) {
+        qa = first;
+        hi = count == 2 && (qa + 1) * kTile < len ? qa + 1 : qa;
         sink_tiles = p.full ? 0 : (p.S + kTile - 1) / kTile;
         lo = p.full ? 0 : max(0, qa * kTile - p.W + 1) / kTile;
         lo_b = p.full ? 0 : max(0, (qa + 1) * kTile - p.W + 1) / kTile;
@@ -410,21 +408,22 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
     if (warp == 8 && lane < 4) fetch_map(lane == 0 ? &p.tm_q : lane == 1 ? &p.tm_k : lane == 2 ? &p.tm_v : &p.tm_out);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
-    // the query tiles with most keys first
-    const int heads = p.B * p.hq;
-    const int pair = (p.n_t + 1) / 2 - 1 - int(blockIdx.x) / heads;
-    const int b = int(blockIdx.x) % heads / p.hq, h = int(blockIdx.x) % p.hq, g = h / p.G;
-    const int len = length_of(p, b), i0 = 2 * pair * kTile;
+    // the query tiles with most keys first; those of the last pairs one by one
+    const int heads = p.B * p.hq, alone = int(blockIdx.x) - p.pairs, count = alone < 0 ? 2 : 1;
+    const int item = alone < 0 ? int(blockIdx.x) : p.pairs + alone / 2;
+    const int first = 2 * ((p.n_t + 1) / 2 - 1 - item / heads) + (alone < 0 ? 0 : 1 - alone % 2);
+    const int b = item % heads / p.hq, h = item % p.hq, g = h / p.G;
+    const int len = length_of(p, b), i0 = first * kTile;
     const int64_t row0 = (int64_t(b) * p.hq + h) * p.Tp;
     if (i0 >= len) {        // no row of a sequence: zeros
-        for (int x = threadIdx.x; x < 2 * kTile * 16; x += kThreads) {
+        for (int x = threadIdx.x; x < count * kTile * 16; x += kThreads) {
             const int t = i0 + x / 16;
             if (t < p.T) *reinterpret_cast<uint4*>(row_at<T>(p.out, b, h, t) + x % 16 * 8) = make_uint4(0, 0, 0, 0);
         }
-        for (int t = i0 + threadIdx.x; t < min(i0 + 2 * kTile, p.Tp); t += kThreads) p.stats[row0 + t] = -CUDART_INF_F;
+        for (int t = i0 + threadIdx.x; t < min(i0 + count * kTile, p.Tp); t += kThreads) p.stats[row0 + t] = -CUDART_INF_F;
         return;
     }
-    const PairTiles tiles(p, pair, len);
+    const PairTiles tiles(p, first, count, len);
     set_up(sh, 4, 1, 1);
     const uint32_t tmem = sh.tmem;
     const Waiter wait{p.status, p.timeout_ns, &sh.abort_flag};
@@ -574,7 +573,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
             arrive_warp(&sh.p_full[x]);
             ++seen;
         }
-        if (qt > tiles.hi) {                // the second tile lies behind the sequence
+        if (x >= count) {                   // another CTA's tile
+        } else if (qt > tiles.hi) {         // the second tile lies behind the sequence
             if (i < p.T)
                 for (int c = 0; c < kTile; c += 8)
                     *reinterpret_cast<uint4*>(row_at<T>(p.out, b, h, i) + c) = make_uint4(0, 0, 0, 0);
@@ -1272,6 +1272,19 @@ void plan_pieces(WindowAttnParams& p, int num_sms) {
     p.items_kv = (p.n_long * p.p_long + (p.n_t - p.n_long) * p.p_short) * p.B * p.n_kv;
 }
 
+// Pairs of query tiles that the forward's CTAs take; those behind them go one
+// tile to a CTA, which takes about 0.8 of a pair's time.  Worth it where pairs
+// would leave half of the SMs or more idle: all of them where there are few
+// (one head of 8192 tokens: 110 us instead of 136; 2 x 8 heads of 1024: 19.5
+// instead of 23.2), and a last wave of equal ones (16 heads of 8192 tokens,
+// window 1024, 3.46 waves: 113 instead of 118).  Without a window the last
+// pairs are short and fill the gaps as they are (32 heads of 4096 tokens: 151.5,
+// and 153 with single tiles at the end).
+void plan_pairs(WindowAttnParams& p, int num_sms) {
+    const int all = (p.n_t + 1) / 2 * p.B * p.hq, rest = p.full ? all : all % num_sms;
+    p.pairs = 2 * rest <= num_sms ? all - rest : all;
+}
+
 int64_t partial_slots(const WindowAttnParams& p) {
     const int64_t bk = int64_t(p.B) * p.n_kv;
     return (p.p_long > 1 ? int64_t(p.n_long) * p.p_long * bk : 0) +
@@ -1310,7 +1323,8 @@ cudaError_t launch(K kernel, const WindowAttnParams& p, dim3 grid, int threads, 
 
 template <typename T>
 int run_forward(const WindowAttnParams& p, cudaStream_t s) {
-    return launch(window_fwd_kernel<T>, p, dim3(unsigned((p.n_t + 1) / 2 * p.B * p.hq)), kThreads, kSmem, s) == cudaSuccess
+    const unsigned items = unsigned(p.pairs + 2 * ((p.n_t + 1) / 2 * p.B * p.hq - p.pairs));
+    return launch(window_fwd_kernel<T>, p, dim3(items), kThreads, kSmem, s) == cudaSuccess
                ? DUO_OK
                : DUO_ERR_CUDA;
 }
@@ -1368,6 +1382,7 @@ int duo_window_attn(const duo_window_attn_desc* d, const duo_heads* q, const duo
     if (duo::device_sms(&sms)) return DUO_ERR_CUDA;
     duo::WindowAttnParams p{};
     duo::fill_params(p, *d, stats, status);
+    duo::plan_pairs(p, sms);
     if (!duo::make_map(&p.tm_q, *q, *d, p.hq) || !duo::make_map(&p.tm_k, *k, *d, p.n_kv) ||
         !duo::make_map(&p.tm_v, *v, *d, p.n_kv) || !duo::make_map(&p.tm_out, *out, *d, p.hq))
         return DUO_ERR_CUDA;

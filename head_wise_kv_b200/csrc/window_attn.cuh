@@ -26,6 +26,7 @@ struct WindowAttnParams {
     int B, hq, n_kv, G, T, Tp, n_t;
     int S, W, full;          // S, W <= T; full: no window
     float scale, scale_log2;
+    int pairs;               // forward: work items of two query tiles; those of one follow
     int n_long;              // key tiles of the first class (those that hold sinks), each in p_long pieces;
     int p_long, p_short;     // the others in p_short
     int items_kv;            // work items of the key tiles; those of the query tiles follow

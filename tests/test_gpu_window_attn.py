@@ -371,3 +371,38 @@ def test_a_dimension_of_one_entry_has_any_stride():
     ga = torch.autograd.grad(window_attention(*a, 1, 7), a, g)
     gb = torch.autograd.grad(window_attention(*b, 1, 7), b, g)
     assert all(torch.equal(s, t) for s, t in zip(ga, gb))
+
+
+# enough heads that the forward takes two query tiles to a CTA (the cases above are small: one each), or
+# two for the first and one for the last of them
+MANY = [   # B, hq, n_kv, T, sink, window, lengths
+    (3, 14, 2, 400, 0, None, [400, 129, 257]), (1, 32, 8, 600, 0, None, None), (2, 26, 2, 385, 16, 64, [385, 200]),
+    (4, 44, 4, 130, 4, 33, [130, 0, 129, 1]), (1, 80, 8, 513, 200, 150, [400]),
+]
+
+
+@pytest.mark.parametrize("B,hq,n_kv,T,sink,window,lengths", MANY)
+@pytest.mark.parametrize("dtype,token_major", [(torch.bfloat16, True), (torch.float16, False)])
+def test_many_heads(B, hq, n_kv, T, sink, window, lengths, dtype, token_major):
+    """Values and gradients; and each head alone, whose tiles go one to a CTA, gives the same bits."""
+    from head_wise_kv_b200 import window_attention, window_attention_status
+    q, k, v, g = _make(B, hq, n_kv, T, dtype, token_major, T + 1)
+    got = _run(q, k, v, g, sink, window, lengths)
+    _check(q, k, v, g, got, sink, window, lengths, 128 ** -0.5)
+    le = torch.tensor(lengths, dtype=torch.int32, device=DEV) if lengths is not None else None
+    G = hq // n_kv
+    for h in range(0, hq, 5):
+        one = window_attention(q[:, h:h + 1], k[:, h // G:h // G + 1], v[:, h // G:h // G + 1], sink, window, lengths=le)
+        assert torch.equal(one, got[0][:, h:h + 1])
+    assert window_attention_status(DEV) == 0
+
+
+@pytest.mark.parametrize("B,hq,n_kv,T,sink,window", [(4, 44, 4, 130, 4, 33), (2, 26, 2, 385, 0, None)])
+def test_garbage_behind_sequences_of_many_heads(B, hq, n_kv, T, sink, window):
+    q, k, v, g = _make(B, hq, n_kv, T, torch.bfloat16, False, 5)
+    lengths = [max(T - 61 * b, 0) for b in range(B)]
+    clean = _run(q, k, v, g, sink, window, lengths)
+    for x in (q, k, v, g):
+        for b, n in enumerate(lengths):
+            x[b, :, n:] = float("nan")
+    assert all(torch.equal(a, b) for a, b in zip(clean, _run(q, k, v, g, sink, window, lengths)))
