@@ -159,7 +159,8 @@ class DuoKVCache:
         every sequence, behind its len_before (int32 [batch]; 0 starts a new
         request): pages on a cache with ``manage_pages``, and the map of the
         step's tokens in ``tokens`` (a TokenMap, returned); see
-        duo_kv_reserve.  Without ``tokens`` only the pages are reserved and
+        duo_kv_reserve.  len_before may be ``tokens.len_after`` (lengths that
+        advance in place).  Without ``tokens`` only the pages are reserved and
         len_after (int32 [batch]) is returned."""
         return self._calls.reserve(len_before, n_new, tokens)
 

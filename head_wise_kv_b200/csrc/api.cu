@@ -681,6 +681,16 @@ int duo_kv_reserve(duo_kv* kv, const int32_t* len_before, const int32_t* n_new, 
                             static_cast<const void*>(seq), static_cast<const void*>(pos)})
         if (reinterpret_cast<uintptr_t>(ptr) & 3) return DUO_ERR_ALIGNMENT;
     if (reinterpret_cast<uintptr_t>(slot) & 7) return DUO_ERR_ALIGNMENT;
+    // a sequence's thread reads its lengths before it writes, so in place is well; any other overlap is a race
+    const size_t B = size_t(kv->desc.batch), T = size_t(map_tokens);
+    const struct { const void* at; size_t bytes; } written[5] = {
+        {len_after, 4 * B}, {cu, cu ? 4 * (B + 1) : 0}, {seq, 4 * T}, {pos, 4 * T}, {slot, 8 * T}};
+    for (const int32_t* in : {len_before, n_new})
+        for (const auto& w : written) {
+            const uintptr_t a = reinterpret_cast<uintptr_t>(in), b = reinterpret_cast<uintptr_t>(w.at);
+            if (in && w.bytes > 0 && a < b + w.bytes && b < a + 4 * B && !(in == len_after && w.at == len_after))
+                return DUO_ERR_INVALID_ARG;
+        }
     if (!on_device(kv)) return DUO_ERR_INVALID_ARG;
     duo::ReserveParams p{};
     if (kv->page_tokens > 0)

@@ -110,8 +110,10 @@ __device__ __forceinline__ Request request_of(const ReserveParams& p, int b) {
     return r;
 }
 
-__device__ __forceinline__ void write_map(const ReserveParams& p, int t, int b, int start) {
-    const int pos = p.len_before[b] + (t - start);
+// Entry t of the map, a token of sequence b, whose entries are cu[b] .. cu[b + 1] - 1.  Its position comes
+// from what the step wrote and not from len_before: len_after may be the same array.
+__device__ __forceinline__ void write_map(const ReserveParams& p, const int32_t* cu, int t, int b) {
+    const int pos = p.len_after[b] - (cu[b + 1] - t);
     p.seq[t] = b;
     p.pos[t] = pos;
     int64_t slot;
@@ -278,8 +280,7 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(const __grid_constant
                 write_no_token(p, t);
                 continue;
             }
-            const int b = last_at_most<int32_t>(cu, p.B, t);
-            write_map(p, t, b, cu[b]);
+            write_map(p, cu, t, last_at_most<int32_t>(cu, p.B, t));
         }
     }
 }
@@ -296,8 +297,7 @@ __global__ void __launch_bounds__(kMapThreads) map_kernel(const __grid_constant_
         write_no_token(p, t);
         return;
     }
-    const int b = last_at_most<int32_t>(p.cu, p.B, t);
-    write_map(p, t, b, p.cu[b]);
+    write_map(p, p.cu, t, last_at_most<int32_t>(p.cu, p.B, t));
 }
 
 __global__ void pages_init_kernel(PageState st, int64_t entries, int64_t B, int64_t num_pages) {

@@ -629,6 +629,8 @@ DUO_API int duo_kv_pages_view_get(const duo_kv* kv, duo_kv_pages_view* out);
  *   map_tokens: entries of seq, pos and slot (0 with all three and cu NULL:
  *     no map);
  *   len_after: [batch] = len_before + n_new where served, else len_before;
+ *     may be len_before or n_new itself (lengths that advance in place), but
+ *     no array that is written overlaps an input in another way;
  *   cu: [batch + 1], tokens served before each sequence: sequence b's are
  *     entries cu[b] .. cu[b + 1] - 1 of the map, in position order;
  *   seq, pos (int32), slot (int64): [map_tokens] as in duo_token_map,

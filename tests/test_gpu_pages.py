@@ -178,3 +178,49 @@ def test_refusals():
         c.reserve(z)
     with pytest.raises(ValueError):
         TokenMap(0, 4, DEV)
+
+
+@pytest.mark.parametrize("B,paged", [(3, True), (5, False), (2100, True)])
+def test_lengths_that_advance_in_place(B, paged):
+    """len_before is the map's own len_after: short maps (written by the block) and long ones (a second launch)."""
+    from head_wise_kv_b200 import DuoKVCache, TokenMap
+    cap, pages = 4096, 4 * B + 60
+    c = _cache(B, pages) if paged else DuoKVCache(1, B, 1, 1, 128, 0, 1, cap, [[1]], device=DEV)
+    o = O.PageTables(B, pages, 256, 16, cap)
+    rng = np.random.default_rng(B)
+    host, state = [0] * B, None
+    for step, top in enumerate((3, 1, 2000 if B < 9 else 5, 2, 1500 if B < 9 else 4)):
+        new = [int(n) for n in rng.integers(0, top + 1, B)]
+        T = max(sum(new) + 3, 1)
+        m = TokenMap(B, T, DEV)
+        if state is not None:
+            m.len_after.copy_(state)
+        want = o.reserve(host, new, T)
+        assert c.reserve(m.len_after, _i32(new), m) is m
+        assert not want[5] and c.status() == 0
+        n = sum(new)
+        for got, ref in zip((m.len_after, m.cu, m.seq, m.pos), want):
+            assert np.array_equal(got.cpu().numpy(), ref)
+        slots = want[4] if paged else [b * cap + p if b >= 0 else -1 for b, p in zip(want[2], want[3])]
+        assert np.array_equal(m.slot.cpu().numpy(), slots) and (m.slot[n:] == -1).all()
+        if paged:
+            _state_equal(c, o)
+        host, state = want[0], m.len_after
+    # the counts in the array that the lengths go to
+    m.len_after.fill_(1)
+    c.reserve(_i32(host), m.len_after, m)
+    assert m.len_after.tolist()[:2] == [h + 1 for h in host[:2]]
+
+
+def test_arrays_that_overlap_in_another_way_are_refused():
+    from head_wise_kv_b200 import DuoError, TokenMap
+    c = _cache(3, 9)
+    m, lens = TokenMap(3, 8, DEV), _i32([0, 0, 0])
+    shifted = TokenMap(3, 8, DEV)
+    both = _i32([0, 0, 0, 0])
+    shifted.len_after = both[1:]
+    for args in ((both[:3], None, shifted), (lens, both[:3], shifted), (m.cu[1:], None, m), (m.seq[2:5], None, m),
+                 (lens, m.pos[:3], m), (lens, m.slot.view(torch.int32)[13:], m)):
+        with pytest.raises(DuoError):
+            c.reserve(*args)
+    assert c.status() == 0 and c.page_state()["held"].tolist() == [0, 0, 0]
