@@ -312,7 +312,8 @@ class DuoKVCache:
         the projections, token-major, strided or parts of one tensor.
         tokens (a TokenMap): a ragged batch, q [T][Hq][d], k and v
         [T][n_kv][d] with T = tokens.max_tokens.  Without it: a padded batch
-        [B][n][heads][d] and n_new int32 [B] (<= n).  len_before: int32 [B].
+        [B][n][heads][d] and n_new int32 [B] (<= n).  len_before: int32 [B]
+        (with a map, tokens.len_after will do).
         q may be None (keys and values only).  Returns the rotated queries
         (contiguous, in ``out`` if given, which lies apart from q, k and v;
         rows without a token stay as they were, zero where out is new)."""

@@ -567,7 +567,10 @@ typedef struct {
  *     be NULL with q_out NULL: keys and values only);
  *   len_before: device int32 [batch], tokens held before the step;
  *   map != NULL: n_tokens rows, row t is the map's token t; n_new NULL; the
- *     tokens of a sequence are those at len_before[b] .. len_after[b] - 1;
+ *     tokens of a sequence are those at len_before[b] .. len_after[b] - 1
+ *     (len_before may be map->len_after, where duo_kv_reserve advanced the
+ *     lengths in place: the positions are the map's, and a sequence whose
+ *     token 0 is in it starts from empty);
  *   map == NULL: a padded batch of n_tokens rows per sequence, row
  *     b * n_tokens + i holds token i of sequence b, at position
  *     len_before[b] + i; n_new: device int32 [batch] (<= n_tokens) or NULL =

@@ -396,3 +396,35 @@ def test_rotated_queries_over_an_input_are_refused():
     for args in ((x, k, v, x), (x, inside, v, over), (x, k, inside, over)):
         with pytest.raises(ValueError):
             c.append_rope(0, st.rope, *args[:3], zero, out=args[3])
+
+
+def test_lengths_that_advance_in_place():
+    """reserve advances the map's own len_after and append_rope gets that: a request that starts over in a used slot
+    leaves no position of the last one in the ring."""
+    from head_wise_kv_b200 import TokenMap
+    B = 3
+    st = Setup("paged_bf16", B=B, window=9, caches=2)
+    for c in st.caches:
+        c.manage_pages()
+    maps = [TokenMap(B, 60, DEV) for _ in range(2)]
+    lens = torch.zeros(B, dtype=torch.int32, device=DEV)
+    for step, (new, over) in enumerate((([20, 5, 33], None), ([1, 1, 1], None), ([3, 1, 6], [0, 1, 2]), ([2, 0, 1], [1, 2]),
+                                        ([40, 1, 0], [0]))):
+        for b in over or []:        # a new request in this slot
+            lens[b] = 0
+            maps[0].len_after[b] = 0
+        n = torch.tensor(new, dtype=torch.int32, device=DEV)
+        q, k, v = _qkv(st, 60, 70 + step)
+        st.caches[0].reserve(maps[0].len_after, n, maps[0])
+        got = st.caches[0].append_rope(0, st.rope, q, k, v, maps[0].len_after, maps[0])
+        st.caches[1].reserve(lens, n, maps[1])
+        want = st.caches[1].append_rope(0, st.rope, q, k, v, lens, maps[1])
+        lens = maps[1].len_after.clone()
+        assert torch.equal(got, want) and torch.equal(maps[0].len_after, lens)
+        a, b = (c.layer_views(0) for c in st.caches)
+        # a slot whose request has not brought a token yet is not looked at before it does
+        live = lens > 0
+        assert torch.equal(a["positions"][live], b["positions"][live])
+        for name in ("k_retrieval", "v_retrieval", "k_streaming", "v_streaming"):
+            assert _same(a[name], b[name]), name
+    assert st.caches[0].status() == st.caches[1].status() == 0
