@@ -10,16 +10,19 @@
 #include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <c10/util/SmallVector.h>
 #include <torch/csrc/autograd/functions/basic_ops.h>
 #include <torch/csrc/autograd/variable.h>
 #include <torch/extension.h>
 
+#include <algorithm>
 #include <limits>
 #include <mutex>
 #include <optional>
 #include <sstream>
 #include <stdexcept>
 #include <string>
+#include <tuple>
 #include <vector>
 
 #include "duo_kv.h"
@@ -79,6 +82,109 @@ void check_capture(const Tensor& t, const char* name) {
 
 cudaStream_t stream_of(const at::Device& dev) { return c10::cuda::getCurrentCUDAStream(dev.index()).stream(); }
 
+// ------------------------------------------------------------------ overlap
+// A tensor's memory: blocks of `block` bytes at base + the sum of c_k step_k, 0 <= c_k < count_k.
+struct Blocks {
+    int64_t base = 0, block = 0, end = 0;       // end: behind the last byte
+    struct Dim {
+        int64_t step, count;
+    };
+    c10::SmallVector<Dim, 4> dims;              // of more than one entry
+
+    explicit Blocks(const Tensor& t) {
+        if (t.numel() == 0) return;
+        base = int64_t(reinterpret_cast<uintptr_t>(t.data_ptr()));
+        block = t.element_size();
+        end = base + block;
+        for (int64_t i = t.dim() - 1; i >= 0; --i) {
+            if (t.size(i) == 1) continue;
+            const int64_t step = t.stride(i) * t.element_size();
+            end += (t.size(i) - 1) * step;
+            if (step == block && dims.empty())
+                block *= t.size(i);             // the inner dimensions that lie end to end
+            else
+                dims.push_back({step, t.size(i)});
+        }
+    }
+};
+
+// at + the sum of c_k step_k for some lo_k <= c_k <= hi_k lies in [first, last].  Steps are given in falling order, so
+// that few c_k of each come into question where the dimensions nest; a search that grows long says yes.
+struct Term {
+    int64_t step, lo, hi;
+};
+
+bool reaches(const Term* t, size_t n, int64_t at, int64_t first, int64_t last, int& budget) {
+    if (n == 0) return at >= first && at <= last;
+    if (--budget < 0) return true;
+    int64_t lo = 0, hi = 0;                     // of the later ones together
+    for (size_t k = 1; k < n; ++k) {
+        lo += t[k].step * t[k].lo;
+        hi += t[k].step * t[k].hi;
+    }
+    const auto floor_div = [](int64_t a, int64_t b) { return a / b - (a % b < 0); };
+    const int64_t c0 = std::max(t[0].lo, -floor_div(-(first - at - hi), t[0].step));
+    const int64_t c1 = std::min(t[0].hi, floor_div(last - at - lo, t[0].step));
+    for (int64_t c = c0; c <= c1; ++c)
+        if (reaches(t + 1, n - 1, at + c * t[0].step, first, last, budget)) return true;
+    return false;
+}
+
+constexpr int kSearch = 4096;
+
+void in_order(c10::SmallVector<Term, 8>& t) {
+    std::sort(t.begin(), t.end(), [](const Term& a, const Term& b) { return a.step > b.step; });
+}
+
+// Whether two tensors share a byte.
+bool overlap(const Tensor& x, const Tensor& y) {
+    const Blocks a(x), b(y);
+    if (a.block == 0 || b.block == 0 || a.end <= b.base || b.end <= a.base) return false;
+    c10::SmallVector<Term, 8> terms;
+    const auto add = [&](int64_t step, int64_t lo, int64_t hi) {
+        if (step == 0) return;
+        for (Term& t : terms)
+            if (t.step == step) {
+                t.lo += lo;
+                t.hi += hi;
+                return;
+            }
+        terms.push_back({step, lo, hi});
+    };
+    for (const auto& d : a.dims) add(d.step, -(d.count - 1), 0);
+    for (const auto& d : b.dims) add(d.step, 0, d.count - 1);
+    in_order(terms);
+    int budget = kSearch;
+    return reaches(terms.data(), terms.size(), b.base - a.base, -(b.block - 1), a.block - 1, budget);
+}
+
+// Whether two elements of a tensor share a byte.
+bool overlaps_itself(const Tensor& x) {
+    const Blocks a(x);
+    c10::SmallVector<Term, 8> terms;
+    for (const auto& d : a.dims) {
+        if (d.step == 0) return true;
+        terms.push_back({d.step, -(d.count - 1), d.count - 1});
+    }
+    in_order(terms);
+    int budget = kSearch;
+    for (size_t k = 0; k < terms.size(); ++k) {     // the first index in which the two differ
+        Term save = terms[k];
+        terms[k].lo = 1;
+        if (reaches(terms.data() + k, terms.size() - k, 0, -(a.block - 1), a.block - 1, budget)) return true;
+        terms[k] = save;
+    }
+    return false;
+}
+
+// The same elements at the same places.
+bool same_view(const Tensor& x, const Tensor& y) {
+    if (x.data_ptr() != y.data_ptr() || x.sizes() != y.sizes() || x.scalar_type() != y.scalar_type()) return false;
+    for (int64_t i = 0; i < x.dim(); ++i)
+        if (x.size(i) > 1 && x.stride(i) != y.stride(i)) return false;
+    return true;
+}
+
 // ------------------------------------------------------------------ rotary positions
 int rope_dtype(at::ScalarType t) {
     switch (t) {
@@ -89,16 +195,39 @@ int rope_dtype(at::ScalarType t) {
     }
 }
 
-Tensor rope_apply(uintptr_t plan, int64_t d, const Tensor& x, const Tensor& positions, const OptTensor& n_new,
-                  bool transpose, const OptTensor& given) {
-    const int dtype = rope_dtype(x.scalar_type());
-    TORCH_CHECK_TYPE(dtype >= 0, "dtype ", x.scalar_type(), ", expected bfloat16, float16 or float32");
-    const at::Device dev = x.device();
+// A tensor of a launch and where it goes: null where that is made by the call.
+struct RopeTask {
+    const Tensor* x;
+    const Tensor* out;
+    bool rotate;
+};
+
+// In place each thread writes what it has read; any other overlap would be a race.
+void check_apart(const RopeTask* tasks, size_t count) {
+    for (size_t i = 0; i < count; ++i) {
+        const Tensor& out = *tasks[i].out;
+        TORCH_CHECK_VALUE(!overlaps_itself(out), "out must not overlap itself");
+        for (size_t k = 0; k < count; ++k) {
+            TORCH_CHECK_VALUE((k == i && same_view(out, *tasks[i].x)) || !overlap(out, *tasks[k].x),
+                              "out must be x or lie apart from it");
+            TORCH_CHECK_VALUE(k >= i || !overlap(out, *tasks[k].out), "results must lie apart");
+        }
+    }
+}
+
+// One launch over up to three tensors of a batch: their checks, then duo_rope_apply.  Returns the first result.
+Tensor rope_launch(uintptr_t plan, int64_t d, const RopeTask* tasks, size_t tensors, const Tensor& positions,
+                   const OptTensor& n_new, bool transpose) {
+    TORCH_CHECK_VALUE(tensors >= 1 && tensors <= 3, "one to three tensors in a launch");
+    const Tensor& x0 = *tasks[0].x;
+    const int dtype = rope_dtype(x0.scalar_type());
+    TORCH_CHECK_TYPE(dtype >= 0, "dtype ", x0.scalar_type(), ", expected bfloat16, float16 or float32");
+    const at::Device dev = x0.device();
     TORCH_CHECK_VALUE(dev.is_cuda(), "the tensors must be on a CUDA device");
-    TORCH_CHECK_VALUE(x.dim() == 4 && x.size(3) == d, "shape ", shape_of(x.sizes()), ", expected [batch][heads][tokens][", d,
-                      "]");
-    const int64_t B = x.size(0), H = x.size(1), n = x.size(2), top = std::numeric_limits<int32_t>::max();
-    TORCH_CHECK_VALUE(B <= top && H <= top && n <= top, "too large a tensor");
+    for (size_t i = 0; i < tensors; ++i)
+        TORCH_CHECK_VALUE(tasks[i].x->dim() == 4 && tasks[i].x->size(3) == d, "shape ", shape_of(tasks[i].x->sizes()),
+                          ", expected [batch][heads][tokens][", d, "]");
+    const int64_t B = x0.size(0), n = x0.size(2), top = std::numeric_limits<int32_t>::max();
     const bool per_token = positions.dim() == 2;
     TORCH_CHECK_VALUE(positions.scalar_type() == at::kInt && positions.device() == dev && positions.is_contiguous(),
                       "positions must be contiguous int32 on the tensors' device");
@@ -109,35 +238,45 @@ Tensor rope_apply(uintptr_t plan, int64_t d, const Tensor& x, const Tensor& posi
                               n_new->sizes() == at::IntArrayRef({B}),
                           "n_new must be contiguous int32 [", B, "] on the tensors' device");
     const c10::cuda::CUDAGuard guard(dev);
-    Tensor out;
-    if (given) {
-        out = *given;
-        TORCH_CHECK_VALUE(out.sizes() == x.sizes() && out.scalar_type() == x.scalar_type() && out.device() == dev,
-                          "out must have the input's shape, dtype and device");
-    } else {
-        out = n_new ? at::zeros(x.sizes(), x.options()) : at::empty(x.sizes(), x.options());
+    duo_rope_tensor list[3] = {};
+    Tensor made;
+    for (size_t i = 0; i < tensors; ++i) {
+        const Tensor& x = *tasks[i].x;
+        TORCH_CHECK_VALUE(x.scalar_type() == x0.scalar_type() && x.device() == dev && x.size(0) == B && x.size(2) == n,
+                          "tensors of one launch share dtype, device, batch and tokens");
+        TORCH_CHECK_VALUE(B <= top && x.size(1) <= top && n <= top, "too large a tensor");
+        TORCH_CHECK_VALUE(x.stride(3) == 1, "the elements of a head must be contiguous");
+        TORCH_CHECK_VALUE(x.size(1) >= 1 || B * n == 0, "a tensor has at least one head");
+        if (!tasks[i].out) made = n_new ? at::zeros(x.sizes(), x.options()) : at::empty(x.sizes(), x.options());
+        const Tensor& out = tasks[i].out ? *tasks[i].out : made;
+        if (tasks[i].out) {
+            TORCH_CHECK_VALUE(out.sizes() == x.sizes() && out.scalar_type() == x.scalar_type() && out.device() == dev,
+                              "out must have the input's shape, dtype and device");
+            TORCH_CHECK_VALUE(out.stride(3) == 1, "the elements of a head must be contiguous");
+        }
+        duo_rope_tensor& t = list[i];
+        t.in = x.data_ptr();
+        t.out = out.data_ptr();
+        t.heads = int32_t(x.size(1));
+        t.rotate = tasks[i].rotate;
+        for (int k = 0; k < 3; ++k) {     // a dimension of one entry has no stride that matters
+            t.in_stride[k] = x.size(k) > 1 ? x.stride(k) : 0;
+            t.out_stride[k] = x.size(k) > 1 ? out.stride(k) : 0;
+        }
     }
-    TORCH_CHECK_VALUE(x.stride(3) == 1 && out.stride(3) == 1, "the elements of a head must be contiguous");
-    if (given) {       // in place each thread writes what it has read; any other overlap would be a race
-        TORCH_CHECK_VALUE(at::has_internal_overlap(out) != at::MemOverlap::Yes, "out must not overlap itself");
-        TORCH_CHECK_VALUE(at::get_overlap_status(out, x) != at::MemOverlapStatus::Partial,
-                          "out must be x or lie apart from it");
-    }
-    duo_rope_tensor t{};
-    t.in = x.data_ptr();
-    t.out = out.data_ptr();
-    t.heads = int32_t(H);
-    t.rotate = 1;
-    TORCH_CHECK_VALUE(H >= 1 || B * n == 0, "a tensor has at least one head");
-    for (int i = 0; i < 3; ++i) {     // a dimension of one entry has no stride that matters
-        t.in_stride[i] = x.size(i) > 1 ? x.stride(i) : 0;
-        t.out_stride[i] = x.size(i) > 1 ? out.stride(i) : 0;
-    }
-    if (x.numel() == 0) return out;
-    check(duo_rope_apply(reinterpret_cast<const duo_rope*>(plan), dtype, transpose, int32_t(B), int32_t(n), &t, 1,
-                         ints(positions), per_token, ints(n_new), stream_of(dev)),
+    if (tasks[0].out) check_apart(tasks, tensors);
+    const Tensor& first = tasks[0].out ? *tasks[0].out : made;
+    if (x0.numel() == 0) return first;
+    check(duo_rope_apply(reinterpret_cast<const duo_rope*>(plan), dtype, transpose, int32_t(B), int32_t(n), list,
+                         int32_t(tensors), ints(positions), per_token, ints(n_new), stream_of(dev)),
           "duo_rope_apply");
-    return out;
+    return first;
+}
+
+Tensor rope_apply(uintptr_t plan, int64_t d, const Tensor& x, const Tensor& positions, const OptTensor& n_new,
+                  bool transpose, const OptTensor& given) {
+    const RopeTask task{&x, given ? &*given : nullptr, true};
+    return rope_launch(plan, d, &task, 1, positions, n_new, transpose);
 }
 
 // ------------------------------------------------------------------ the cache's calls
@@ -481,6 +620,14 @@ PYBIND11_MODULE(TORCH_EXTENSION_NAME, m) {
         }
     });
     m.def("rope_apply", &rope_apply);
+    m.def("rope_launch", [](uintptr_t plan, int64_t d, const std::vector<std::tuple<Tensor, Tensor, bool>>& tensors,
+                            const Tensor& positions, const OptTensor& n_new, bool transpose) {
+        std::vector<RopeTask> tasks;
+        for (const auto& [x, out, rotate] : tensors) tasks.push_back({&x, &out, rotate});
+        rope_launch(plan, d, tasks.data(), tasks.size(), positions, n_new, transpose);
+    });
+    m.def("overlap", &overlap);
+    m.def("overlaps_itself", &overlaps_itself);
     m.def("check_capture", [](const Tensor& t) { check_capture(t, "x"); });
     py::class_<Cache>(m, "Cache")
         .def(py::init<uintptr_t, int64_t, int64_t, int64_t, int64_t, int64_t>())

@@ -411,7 +411,7 @@ cudaError_t launch_pages_init(const PageState& st, int64_t B, int64_t max_pages,
 cudaError_t launch_reserve(const ReserveParams& p, cudaStream_t s) {
     const cudaError_t e = launch(reserve_kernel, p, 1, kThreads, s);
     if (e != cudaSuccess || !p.cu || p.T <= kMapInBlock) return e;
-    return launch(map_kernel, p, (p.T + kMapThreads - 1) / kMapThreads, kMapThreads, s);
+    return launch(map_kernel, p, (p.T - 1) / kMapThreads + 1, kMapThreads, s);     // no sum that passes 31 bits
 }
 
 cudaError_t launch_share(const ShareParams& p, cudaStream_t s) { return launch(share_kernel, p, 1, kThreads, s); }

@@ -7,7 +7,6 @@ import torch
 from . import _lib as L
 from . import _binding as _b
 
-_DTYPE = {torch.bfloat16: L.DUO_BF16, torch.float16: L.DUO_FP16, torch.float32: L.DUO_FP32}
 _LAYOUT = {"half": L.DUO_ROPE_HALF, "interleaved": L.DUO_ROPE_INTERLEAVED}
 _SCALING = {"none": L.DUO_ROPE_NONE, "linear": L.DUO_ROPE_LINEAR, "ntk": L.DUO_ROPE_NTK, "yarn": L.DUO_ROPE_YARN,
             "bands": L.DUO_ROPE_BANDS, "factors": L.DUO_ROPE_FACTORS}
@@ -55,50 +54,14 @@ class Rope:
         return L.duo_rope_frequencies(self.handle, self.rot_dim)
 
     # ------------------------------------------------------------------ the call
-    def _entry(self, x, out, rotate=1):
-        if x.dim() != 4 or x.shape[3] != self.d:
-            raise ValueError(f"shape {tuple(x.shape)}, expected [batch][heads][tokens][{self.d}]")
-        if out.shape != x.shape or out.dtype != x.dtype or out.device != x.device:
-            raise ValueError("out must have the input's shape, dtype and device")
-        if x.stride(3) != 1 or out.stride(3) != 1:
-            raise ValueError("the elements of a head must be contiguous")
-        # a dimension of one entry has no stride that matters
-        xs, os = ([t.stride(i) if t.shape[i] > 1 else 0 for i in range(3)] for t in (x, out))
-        return L.duo_rope_tensor(x.data_ptr(), out.data_ptr(), x.shape[1], rotate, (L._I64 * 3)(*xs),
-                                 (L._I64 * 3)(*os))
-
     def launch(self, tensors, positions, n_new=None, transpose=False):
         """Rotate (or, with False in third place, only lay out) up to three
         tensors of one batch in one launch: tensors = [(x, out, rotate)], each
-        [batch][heads][tokens][d] by strides, the same dtype and device."""
-        x0 = tensors[0][0]
-        dt = _DTYPE.get(x0.dtype)
-        if dt is None:
-            raise TypeError(f"dtype {x0.dtype}, expected bfloat16, float16 or float32")
-        dev, B, n = x0.device, x0.shape[0], x0.shape[2]
-        if dev.type != "cuda":
-            raise ValueError("the tensors must be on a CUDA device")
-        for x, _, _ in tensors[1:]:
-            if x.dtype != x0.dtype or x.device != dev or x.shape[0] != B or x.shape[2] != n:
-                raise ValueError("tensors of one launch share dtype, device, batch and tokens")
-        per_token = positions.dim() == 2
-        if positions.dtype != torch.int32 or positions.device != dev or not positions.is_contiguous():
-            raise ValueError("positions must be contiguous int32 on the tensors' device")
-        if tuple(positions.shape) != ((B, n) if per_token else (B,)):
-            raise ValueError(f"positions: shape {tuple(positions.shape)}, expected ({B},) or ({B}, {n})")
-        if n_new is not None and (n_new.dtype != torch.int32 or n_new.device != dev or tuple(n_new.shape) != (B,)
-                                  or not n_new.is_contiguous()):
-            raise ValueError(f"n_new must be contiguous int32 [{B}] on the tensors' device")
-        arr = (L.duo_rope_tensor * len(tensors))(*[self._entry(x, o, int(bool(r))) for x, o, r in tensors])
-        if torch.cuda.current_device() == dev.index:
-            self._call(dt, transpose, B, n, arr, positions, per_token, n_new, dev)
-        else:
-            with torch.cuda.device(dev):
-                self._call(dt, transpose, B, n, arr, positions, per_token, n_new, dev)
-
-    def _call(self, dt, transpose, B, n, arr, positions, per_token, n_new, dev):
-        L.duo_rope_apply(self.handle, dt, int(bool(transpose)), B, n, arr, positions.data_ptr(), int(per_token),
-                         n_new.data_ptr() if n_new is not None else None, torch.cuda.current_stream(dev).cuda_stream)
+        [batch][heads][tokens][d] by strides, the same dtype and device.  An
+        out may be its x; otherwise results lie apart from each other and
+        from what is read."""
+        _b.rope_launch(self.handle or 0, self.d, [(x, o, bool(r)) for x, o, r in tensors], positions, n_new,
+                       bool(transpose))
 
     def apply(self, x, positions, n_new=None, transpose=False, out=None):
         """Rotate x ([batch][heads][tokens][d], any strides with contiguous

@@ -224,3 +224,22 @@ def test_arrays_that_overlap_in_another_way_are_refused():
         with pytest.raises(DuoError):
             c.reserve(*args)
     assert c.status() == 0 and c.page_state()["held"].tolist() == [0, 0, 0]
+
+
+def test_the_longest_map():
+    """2^31 - 1 entries: the number of blocks is worked out without passing 31 bits."""
+    from head_wise_kv_b200 import TokenMap
+    T = 2 ** 31 - 1
+    free, _ = torch.cuda.mem_get_info()
+    if free < 40 << 30:
+        pytest.skip("needs 34 GB for the map")
+    c, o = _cache(2, 20), O.PageTables(2, 20, 256, 16, 4096)
+    m = TokenMap(2, T, DEV)
+    m.seq[-3:] = 7
+    c.reserve(_i32([0, 0]), _i32([300, 5]), m)
+    want = o.reserve([0, 0], [300, 5], 400)
+    for got, ref in zip((m.seq, m.pos, m.slot), want[2:5]):
+        assert got[:400].tolist() == ref and (got[-1000:] == -1).all()
+    assert m.len_after.tolist() == [300, 5] and c.status() == 0
+    del m
+    torch.cuda.empty_cache()

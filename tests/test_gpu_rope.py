@@ -200,3 +200,52 @@ def test_out_that_overlaps_is_refused():
     assert torch.equal(flat, keep)
     want = r.apply(x, pos)
     assert r.apply(x, pos, out=x) is not None and torch.equal(x, want)
+
+
+def test_out_within_the_storage_of_a_strided_input():
+    """Parts of one projection: a shifted part races between rows, one that lies apart or the input itself does not."""
+    from head_wise_kv_b200 import Rope
+    r = Rope(128)
+    pos = torch.tensor([3, 900], dtype=torch.int32, device=DEV)
+    qkv = torch.randn(2, 70, 12, 128, device=DEV).to(torch.bfloat16)
+    keep = qkv.clone()
+    q, by_token = qkv.transpose(1, 2), qkv.transpose(1, 2)[:, :4]
+    dense = qkv.view(-1)[:2 * 4 * 70 * 128].view(2, 4, 70, 128)
+    for out in (q[:, 1:5], q.as_strided(by_token.shape, by_token.stride(), 64), dense):
+        with pytest.raises(ValueError, match="apart"):
+            r.apply(by_token, pos, out=out)
+        with pytest.raises(ValueError, match="apart"):
+            r.launch([(by_token, out, True)], pos)
+    with pytest.raises(ValueError, match="itself"):
+        r.apply(by_token, pos, out=torch.empty(2 * 200 * 128, device=DEV, dtype=torch.bfloat16).as_strided(
+            (2, 4, 70, 128), (200 * 128, 64, 256, 1)))
+    other = torch.empty_like(by_token)
+    for tensors in ([(q[:, :4], q[:, 4:8], True), (q[:, 4:8], other, True)],         # one's result is another's input
+                    [(q[:, :4], other, True), (q[:, 4:8], other, True)]):            # one result for two
+        with pytest.raises(ValueError, match="apart"):
+            r.launch(tensors, pos)
+    assert torch.equal(qkv, keep)
+    want = [r.apply(q[:, i:i + 4].contiguous(), pos) for i in (0, 4)]
+    r.apply(q[:, :4], pos, out=q[:, 8:])
+    assert torch.equal(q[:, 8:], want[0]) and torch.equal(q[:, :8], keep.transpose(1, 2)[:, :8])
+    r.launch([(q[:, :4], q[:, :4], True), (q[:, 4:8], q[:, 4:8], True)], pos)        # in place
+    assert torch.equal(q[:, :4], want[0]) and torch.equal(q[:, 4:8], want[1])
+
+
+def test_launch_refusals():
+    from head_wise_kv_b200 import Rope
+    r = Rope(128)
+    x = torch.zeros(2, 4, 6, 128, dtype=torch.bfloat16, device=DEV)
+    pos = torch.zeros(2, dtype=torch.int32, device=DEV)
+
+    def new(t):
+        return torch.empty_like(t)
+    for tensors in ([], [(x, new(x), True)] * 4, [(x.cpu(), new(x), True)], [(x, new(x), True), (x[:, :, :3], new(x[:, :, :3]), True)],
+                    [(x, new(x), True), (x.half(), new(x.half()), True)], [(x, new(x)[:, :3], True)],
+                    [(x[..., :64], new(x[..., :64]), True)]):
+        with pytest.raises(ValueError):
+            r.launch(tensors, pos)
+    with pytest.raises(TypeError):
+        r.launch([(x.double(), new(x.double()), True)], pos)
+    with pytest.raises(ValueError):
+        r.launch([(x, new(x), True)], pos[:1])

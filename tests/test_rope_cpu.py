@@ -3,9 +3,12 @@ against the oracle's formulas, the oracle's rotation against its definition,
 the oracle's page tables on hand-made cases, and the refusals that need no
 device."""
 import ctypes
+import itertools
+import random
 
 import numpy as np
 import pytest
+import torch
 
 from oracle import duo_oracle as O
 
@@ -171,3 +174,42 @@ def test_oracle_fork_shares_full_pages():
     # going back into a shared page is refused
     assert t.reserve([0, 10, 6], [0, 0, 1])[5] == {"shared"}
     assert not t.fork(1, 0, 16)          # the source holds fewer pages
+
+
+# ------------------------------------------------------------ overlap of strided tensors
+def _bytes_of(t):
+    size, places = t.element_size(), set()
+    for index in itertools.product(*[range(n) for n in t.shape]):
+        at = t.data_ptr() + size * sum(i * s for i, s in zip(index, t.stride()))
+        places.update(range(at, at + size))
+    return places
+
+
+def test_overlap_is_that_of_the_bytes():
+    """Random strided tensors of two element sizes in one storage against the sets of their bytes."""
+    from head_wise_kv_b200 import _binding
+    rng = random.Random(0)
+    base = torch.zeros(400)
+    for _ in range(1500):
+        x, y = (torch.as_strided(rng.choice([base, base.view(torch.bfloat16)]),
+                                 [rng.choice([0, 1, 2, 3, 4, 4, 4]) if rng.random() < 0.1 else rng.randint(1, 4) for _ in range(3)],
+                                 [rng.choice([0, 1, 2, 3, 4, 5, 6, 8, 12, 16, 24, 30, 37]) for _ in range(3)],
+                                 rng.randint(0, 60)) for _ in range(2))
+        bx, by = _bytes_of(x), _bytes_of(y)
+        assert _binding.overlap(x, y) == _binding.overlap(y, x) == bool(bx & by), (x.shape, x.stride(), y.shape, y.stride())
+        assert _binding.overlaps_itself(x) == (len(bx) < x.numel() * x.element_size()), (x.shape, x.stride())
+
+
+def test_overlap_of_a_projections_parts():
+    from head_wise_kv_b200 import _binding
+    qkv = torch.zeros(2, 500, 12, 128, dtype=torch.bfloat16)
+    q, k, v = qkv.split([8, 2, 2], 2)
+    for a, b in ((q, k), (q, v), (k, v), (q.transpose(1, 2), k.transpose(1, 2)), (qkv[:, :200], qkv[:, 200:])):
+        assert not _binding.overlap(a, b) and not _binding.overlap(b, a)
+    flat = qkv.view(-1)
+    inside = flat[12 * 128 * 3 + 5: 12 * 128 * 3 + 5 + 1024].view(8, 128)
+    for a, b in ((qkv[:, :, :4], qkv[:, :, 1:5]), (qkv[:, :4], qkv[:, 1:5]), (q, inside), (q, flat[:1024]), (k, qkv)):
+        assert _binding.overlap(a, b) and _binding.overlap(b, a)
+    assert not _binding.overlap(k, flat[:1024]) and not _binding.overlap(k, flat[1280:1536])
+    assert _binding.overlaps_itself(q.expand(2, 500, 8, 128)[:1, :1].expand(3, 4, 8, 128))
+    assert not any(_binding.overlaps_itself(t) for t in (q, k, v, q.transpose(1, 2)))
