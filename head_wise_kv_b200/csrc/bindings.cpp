@@ -5,7 +5,6 @@
 // ctypes cost more than that (8 to 15 us a call, 200 us for a small
 // attention's forward and backward).  Nothing is computed here: every step of
 // the path runs in the library's kernels (duo_kv.h).
-#include <ATen/MemoryOverlap.h>
 #include <ATen/core/grad_mode.h>
 #include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAGuard.h>
@@ -353,11 +352,8 @@ struct Cache {
             shape.push_back(d);
             if (given) {
                 need(*given, "out", at::kBFloat16, shape, dev);
-                for (const Tensor& in : {*q, k, v}) {
-                    const auto lap = at::get_overlap_status(*given, in);
-                    TORCH_CHECK_VALUE(lap != at::MemOverlapStatus::Partial && lap != at::MemOverlapStatus::Full,
-                                      "out must lie apart from q, k and v");
-                }
+                TORCH_CHECK_VALUE(!overlap(*given, *q) && !overlap(*given, k) && !overlap(*given, v),
+                                  "out must lie apart from q, k and v");
                 out = given;
             } else {        // rows without a token are zero where out is new
                 out = ragged || n_new ? at::zeros(shape, k.options()) : at::empty(shape, k.options());

@@ -428,3 +428,29 @@ def test_lengths_that_advance_in_place():
         for name in ("k_retrieval", "v_retrieval", "k_streaming", "v_streaming"):
             assert _same(a[name], b[name]), name
     assert st.caches[0].status() == st.caches[1].status() == 0
+
+
+def test_rotated_queries_within_a_projection_are_refused():
+    """q, k and v as parts of one projection, and an out inside its storage; beside it, it is accepted."""
+    from head_wise_kv_b200 import TokenMap
+    st = Setup("bf16", B=2, caches=1)
+    c, heads = st.caches[0], st.hq + 2 * st.n_kv
+    pool = torch.randn(60 * heads * 128, device=DEV).to(torch.bfloat16)
+    keep, before = pool.clone(), c.buf.clone()
+    zero = torch.zeros(2, dtype=torch.int32, device=DEV)
+    m = TokenMap(2, 10, DEV)
+    m.seq[:3], m.len_after[0] = 0, 3
+    m.pos[:3].copy_(torch.arange(3))
+    q, k, v = pool[10 * 128: 10 * 128 + 10 * heads * 128].view(10, heads, 128).split([st.hq, st.n_kv, st.n_kv], 1)
+    n = 10 * st.hq * 128
+    for start in (0, 128 * 5, 10 * 128, 100 * 128):
+        with pytest.raises(ValueError, match="apart"):
+            c.append_rope(0, st.rope, q, k, v, zero, m, out=pool[start:start + n].view(10, st.hq, 128))
+    q2, k2, v2 = pool[:20 * heads * 128].view(2, 10, heads, 128).split([st.hq, st.n_kv, st.n_kv], 2)
+    with pytest.raises(ValueError, match="apart"):
+        c.append_rope(0, st.rope, q2, k2, v2, zero, out=pool[n:3 * n].view(2, 10, st.hq, 128))
+    assert torch.equal(pool, keep) and torch.equal(c.buf, before)
+    start = 20 * heads * 128
+    got = c.append_rope(0, st.rope, q, k, v, zero, m, out=pool[start:start + n].view(10, st.hq, 128))
+    want = c.append_rope(0, st.rope, q, k, v, zero, m)
+    assert torch.equal(got[:3], want[:3]) and torch.equal(got[3:].reshape(-1), keep[start + 3 * st.hq * 128:start + n])
