@@ -325,8 +325,9 @@ class DuoKVCache:
         v [B][n_kv][d], strided or parts of one tensor): rotate at positions
         len_before, append, and decode over lengths (int32 [B], =
         len_before + 1); see duo_decode_step_rope.  q_rot: bf16 [B][Hq][d]
-        scratch for the rotated queries (allocated if not given).  Returns
-        fp32 out [B][Hq][d] (and lse [B][Hq] if asked)."""
+        scratch for the rotated queries (allocated if not given; may be q).
+        q_rot, out and lse lie apart from each other and from q, k and v.
+        Returns fp32 out [B][Hq][d] (and lse [B][Hq] if asked)."""
         return self._calls.step_rope(layer, rope.handle or 0, rope.d, q, k, v, len_before, lengths, float(scale), out,
                                      lse, want_lse, q_rot, self._ws)
 

@@ -415,6 +415,16 @@ struct Cache {
         if (given_rot) need(*given_rot, "q_rot", at::kBFloat16, {B, hq, d}, dev);
         if (given_out) need(*given_out, "out", at::kFloat, {B, hq, d}, dev);
         if (given_lse) need(*given_lse, "lse", at::kFloat, {B, hq}, dev);
+        // rotated in place each thread writes what it has read; the decode starts while the append runs
+        const OptTensor* const given[3] = {&given_rot, &given_out, &given_lse};
+        for (int i = 0; i < 3; ++i) {
+            if (!*given[i]) continue;
+            const Tensor& t = **given[i];
+            TORCH_CHECK_VALUE(((i == 0 && same_view(t, q)) || !overlap(t, q)) && !overlap(t, k) && !overlap(t, v),
+                              "out, lse and q_rot must lie apart from q, k and v (but q_rot may be q)");
+            for (int j = 0; j < i; ++j)
+                TORCH_CHECK_VALUE(!*given[j] || !overlap(t, **given[j]), "out, lse and q_rot must lie apart");
+        }
         const auto fp32 = q.options().dtype(at::kFloat);
         const Tensor rot = given_rot ? *given_rot : at::empty({B, hq, d}, q.options());
         const Tensor out = given_out ? *given_out : at::empty({B, hq, d}, fp32);

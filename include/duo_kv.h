@@ -588,7 +588,8 @@ DUO_API int duo_kv_append_rope(duo_kv* kv, int32_t layer, const duo_rope* rope, 
 /* One decode step of one layer from the projections' outputs: the result is
  * that of duo_kv_append_rope (padded, one token per sequence) into q_rot
  * ([batch][num_q_heads][d] bf16, caller's scratch), then duo_decode_attn on
- * q_rot.  As in duo_decode_step the attention kernel reads ahead of the
+ * q_rot, which may be q where that is contiguous; q_rot, out and lse lie
+ * apart from each other and from the rows.  As in duo_decode_step the attention kernel reads ahead of the
  * append (head_dim 128, len[b] = len_before[b] + 1 for every sequence); it
  * waits for the rotated queries before its first product. */
 DUO_API int duo_decode_step_rope(duo_kv* kv, int32_t layer, const duo_rope* rope, const duo_rows* q,

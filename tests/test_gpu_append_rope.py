@@ -454,3 +454,30 @@ def test_rotated_queries_within_a_projection_are_refused():
     got = c.append_rope(0, st.rope, q, k, v, zero, m, out=pool[start:start + n].view(10, st.hq, 128))
     want = c.append_rope(0, st.rope, q, k, v, zero, m)
     assert torch.equal(got[:3], want[:3]) and torch.equal(got[3:].reshape(-1), keep[start + 3 * st.hq * 128:start + n])
+
+
+def test_a_steps_results_over_its_inputs_are_refused():
+    """q_rot over a part of the projection, or over out; rotating in place is accepted."""
+    st = Setup("bf16", B=2)
+    heads = st.hq + 2 * st.n_kv
+    pool = torch.randn(2 * heads * 128 + 4096, device=DEV).to(torch.bfloat16)
+    keep, before = pool.clone(), st.caches[0].buf.clone()
+    q, k, v = pool[:2 * heads * 128].view(2, heads, 128).split([st.hq, st.n_kv, st.n_kv], 1)
+    n = 2 * st.hq * 128
+    zero, one = torch.zeros(2, dtype=torch.int32, device=DEV), torch.ones(2, dtype=torch.int32, device=DEV)
+    scratch = torch.zeros(4 * n, device=DEV)
+
+    def step(c, q, **kw):
+        return c.step_rope(0, st.rope, q, k, v, zero, one, 0.1, **kw)
+    rot, out = scratch[:n // 2].view(torch.bfloat16).view(2, st.hq, 128), scratch[:n].view(2, st.hq, 128)
+    lse = scratch[n - 5:n - 5 + 2 * st.hq].view(2, st.hq)
+    part = pool.view(torch.float32)[:n].view(2, st.hq, 128)
+    for kw in (dict(q_rot=pool[:n].view(2, st.hq, 128)), dict(q_rot=pool[n:2 * n].view(2, st.hq, 128)), dict(out=part),
+               dict(lse=part.view(-1)[400:400 + 2 * st.hq].view(2, st.hq)), dict(q_rot=rot, out=out), dict(out=out, lse=lse)):
+        with pytest.raises(ValueError, match="apart"):
+            step(st.caches[0], q, **kw)
+    assert torch.equal(pool, keep) and torch.equal(st.caches[0].buf, before)
+    dense = q.contiguous()
+    want = step(st.caches[0], dense, q_rot=rot)
+    assert torch.equal(step(st.caches[1], dense, q_rot=dense), want) and torch.equal(dense, rot)
+    assert torch.equal(st.caches[0].buf, st.caches[1].buf)
