@@ -64,8 +64,8 @@ class Rope:
                        bool(transpose))
 
     def apply(self, x, positions, n_new=None, transpose=False, out=None):
-        """Rotate x ([batch][heads][tokens][d], any strides with contiguous
-        heads; bf16, fp16 or fp32).  positions: int32 [batch] (token i at
+        """Rotate x ([batch][heads][tokens][d], any strides in steps of 16
+        bytes with contiguous heads; bf16, fp16 or fp32).  positions: int32 [batch] (token i at
         positions[b] + i) or [batch][tokens].  n_new: int32 [batch], only so
         many tokens of each sequence; the rest of out stays as it was (zero
         where out is new).  transpose: the transposed map, i.e. the gradient.
@@ -94,6 +94,6 @@ class _RopeFunction(torch.autograd.Function):
         positions, *rest = ctx.saved_tensors
         if grad.stride(3) != 1 or any(s * grad.element_size() % 16 for s in grad.stride()[:3]) or \
                 grad.data_ptr() % 16:
-            grad = grad.contiguous()
+            grad = grad.clone(memory_format=torch.contiguous_format)     # also where it is contiguous but starts askew
         return ctx.rope._apply(grad, positions, rest[0] if ctx.has_count else None, not ctx.transposed,
                                None), None, None, None, None

@@ -249,3 +249,16 @@ def test_launch_refusals():
         r.launch([(x.double(), new(x.double()), True)], pos)
     with pytest.raises(ValueError):
         r.launch([(x, new(x), True)], pos[:1])
+
+
+def test_gradient_that_starts_askew():
+    """A contiguous gradient whose storage no 16-byte load may start at: the part of a concatenation."""
+    from head_wise_kv_b200 import Rope
+    r = Rope(64)
+    pos = torch.tensor([5, 8], dtype=torch.int32, device=DEV)
+    for dtype in (torch.float32, torch.bfloat16):
+        x = torch.randn(2, 3, 4, 64, device=DEV).to(dtype).requires_grad_()
+        w = torch.randn(1 + x.numel(), device=DEV).to(dtype)
+        joined = torch.cat([torch.zeros(1, device=DEV, dtype=dtype), r.apply(x, pos).flatten()])
+        grad, = torch.autograd.grad(joined, x, w)
+        assert torch.equal(grad, r.apply(w[1:].clone().view(x.shape), pos, transpose=True))
