@@ -12,6 +12,7 @@
 #include <c10/util/SmallVector.h>
 #include <torch/csrc/autograd/functions/basic_ops.h>
 #include <torch/csrc/autograd/variable.h>
+#include <torch/csrc/jit/frontend/tracer.h>
 #include <torch/extension.h>
 
 #include <algorithm>
@@ -63,6 +64,17 @@ void need(const Tensor& t, const char* name, at::ScalarType type, at::IntArrayRe
 
 const int32_t* ints(const Tensor& t) { return static_cast<const int32_t*>(t.data_ptr()); }
 const int32_t* ints(const OptTensor& t) { return t ? ints(*t) : nullptr; }
+
+// What reads a tensor's memory alone loses what rides along with it: a forward-mode tangent, or the
+// operations that a trace records.  Refused instead of left out without a word.
+void check_plain(const Tensor& t, const char* name) {
+    TORCH_CHECK_NOT_IMPLEMENTED(!t._fw_grad(0).defined(), name,
+                                ": forward-mode derivatives are not implemented, the tangent would be lost");
+}
+
+void check_not_traced(const char* call) {
+    TORCH_CHECK_NOT_IMPLEMENTED(!torch::jit::tracer::isTracing(), call, " cannot be traced: the trace would hold an empty result");
+}
 
 // A backward pass captured into a graph must not meet a leaf whose gradient
 // node lives on another stream (an eager graph of the same leaf keeps it): the
@@ -217,7 +229,12 @@ void check_apart(const RopeTask* tasks, size_t count) {
 // One launch over up to three tensors of a batch: their checks, then duo_rope_apply.  Returns the first result.
 Tensor rope_launch(uintptr_t plan, int64_t d, const RopeTask* tasks, size_t tensors, const Tensor& positions,
                    const OptTensor& n_new, bool transpose) {
+    check_not_traced("Rope.apply");
     TORCH_CHECK_VALUE(tensors >= 1 && tensors <= 3, "one to three tensors in a launch");
+    for (size_t i = 0; i < tensors; ++i) {
+        check_plain(*tasks[i].x, "x");
+        if (tasks[i].out) check_plain(*tasks[i].out, "out");
+    }
     const Tensor& x0 = *tasks[0].x;
     const int dtype = rope_dtype(x0.scalar_type());
     TORCH_CHECK_TYPE(dtype >= 0, "dtype ", x0.scalar_type(), ", expected bfloat16, float16 or float32");
@@ -296,6 +313,13 @@ duo_rows rows_of(const Tensor& t, const char* name, int64_t heads, int64_t d, at
                     heads > 1 ? t.stride(n) : 0};
 }
 
+void check_rows(const char* call, const OptTensor& q, const Tensor& k, const Tensor& v) {
+    check_not_traced(call);
+    if (q) check_plain(*q, "q");
+    check_plain(k, "k");
+    check_plain(v, "v");
+}
+
 struct Cache {
     duo_kv* kv;
     at::Device dev;
@@ -313,6 +337,7 @@ struct Cache {
                           const Tensor& len_before, const py::object& tokens, const OptTensor& n_new,
                           const OptTensor& given) const {
         TORCH_CHECK_VALUE(rope_d == d, "rope of head_dim ", rope_d, ", expected ", d);
+        check_rows("append_rope", q, k, v);
         duo_token_map map{};
         const bool ragged = !tokens.is_none();
         std::vector<int64_t> lead;
@@ -407,6 +432,7 @@ struct Cache {
                          const Tensor& len_before, const Tensor& lengths, double scale, const OptTensor& given_out,
                          const OptTensor& given_lse, bool want_lse, const OptTensor& given_rot, const Tensor& ws) const {
         TORCH_CHECK_VALUE(rope_d == d, "rope of head_dim ", rope_d, ", expected ", d);
+        check_rows("step_rope", q, k, v);
         const duo_rows qr = rows_of(q, "q", hq, d, {B}, dev), kr = rows_of(k, "k", n_kv, d, {B}, dev),
                        vr = rows_of(v, "v", n_kv, d, {B}, dev);
         need(len_before, "len_before", at::kInt, {B}, dev);
@@ -577,6 +603,8 @@ Tensor window_attention(const Tensor& q, const Tensor& k, const Tensor& v, int64
                         const OptTensor& lengths, std::optional<double> given_scale) {
     const Tensor* in[3] = {&q, &k, &v};
     const char* names[3] = {"q", "k", "v"};
+    check_not_traced("window_attention");
+    for (int i = 0; i < 3; ++i) check_plain(*in[i], names[i]);
     for (int i = 0; i < 3; ++i) {
         const Tensor& t = *in[i];
         TORCH_CHECK_TYPE((t.scalar_type() == at::kBFloat16 || t.scalar_type() == at::kHalf) &&
@@ -634,7 +662,11 @@ PYBIND11_MODULE(TORCH_EXTENSION_NAME, m) {
     });
     m.def("overlap", &overlap);
     m.def("overlaps_itself", &overlaps_itself);
-    m.def("check_capture", [](const Tensor& t) { check_capture(t, "x"); });
+    m.def("check_recorded", [](const Tensor& t) {       // what an autograd function of Python's checks first
+        check_not_traced("Rope.apply");
+        check_plain(t, "x");
+        check_capture(t, "x");
+    });
     py::class_<Cache>(m, "Cache")
         .def(py::init<uintptr_t, int64_t, int64_t, int64_t, int64_t, int64_t>())
         .def("append_rope", &Cache::append_rope)

@@ -69,11 +69,12 @@ class Rope:
         positions[b] + i) or [batch][tokens].  n_new: int32 [batch], only so
         many tokens of each sequence; the rest of out stays as it was (zero
         where out is new).  transpose: the transposed map, i.e. the gradient.
-        out may be x (in place).  Differentiable in x where out is not given."""
+        out may be x (in place).  Differentiable in x (backward mode) where
+        out is not given."""
         if x.requires_grad and torch.is_grad_enabled():
             if out is not None:
                 raise ValueError("out cannot be given where a gradient is recorded")
-            _b.check_capture(x)
+            _b.check_recorded(x)
             return _RopeFunction.apply(x, positions, n_new, self, bool(transpose))
         return self._apply(x, positions, n_new, transpose, out)
 

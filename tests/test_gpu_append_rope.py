@@ -481,3 +481,22 @@ def test_a_steps_results_over_its_inputs_are_refused():
     want = step(st.caches[0], dense, q_rot=rot)
     assert torch.equal(step(st.caches[1], dense, q_rot=dense), want) and torch.equal(dense, rot)
     assert torch.equal(st.caches[0].buf, st.caches[1].buf)
+
+
+def test_tangents_are_refused():
+    import torch.autograd.forward_ad as fwAD
+    st = Setup("bf16", B=2, caches=1)
+    c = st.caches[0]
+    before = c.buf.clone()
+    q, k, v = (t.contiguous() for t in _qkv(st, 2, 5))
+    zero, one = torch.zeros(2, dtype=torch.int32, device=DEV), torch.ones(2, dtype=torch.int32, device=DEV)
+    with fwAD.dual_level():
+        dual = [fwAD.make_dual(t, torch.ones_like(t)) for t in (q, k, v)]
+        for i in range(3):
+            x = [dual[j] if j == i else t for j, t in enumerate((q, k, v))]
+            for call in (lambda: c.step_rope(0, st.rope, *x, zero, one, 0.1),
+                         lambda: c.append_rope(0, st.rope, *[t[:, None] for t in x], zero),
+                         lambda: c.prefill_rope(0, st.rope, *[t[:, None] for t in x], zero, 0.1)):
+                with pytest.raises(NotImplementedError, match="forward-mode"):
+                    call()
+    assert torch.equal(c.buf, before)

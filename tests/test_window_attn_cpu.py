@@ -123,3 +123,26 @@ def test_python_refusals():
         window_attention(x.float(), x, x)
     with pytest.raises(TypeError):
         window_attention([1], x, x)
+
+
+def test_tangents_and_traces_are_refused():
+    """A result that reads memory alone would lose a forward-mode tangent, and a trace would record nothing."""
+    import torch.autograd.forward_ad as fwAD
+    from head_wise_kv_b200 import Rope, window_attention
+    rope, pos = Rope(128), torch.zeros(1, dtype=torch.int32)
+    x = torch.zeros(1, 2, 3, 128, dtype=torch.bfloat16)
+    with fwAD.dual_level():
+        dual = fwAD.make_dual(x, torch.ones_like(x))
+        for call in (lambda: window_attention(dual, x, x), lambda: window_attention(x, x, dual), lambda: rope.apply(dual, pos),
+                     lambda: rope.apply(dual.requires_grad_(), pos), lambda: rope.apply(x, pos, out=dual),
+                     lambda: rope.launch([(x, x, True), (dual, x, False)], pos)):
+            with pytest.raises(NotImplementedError, match="forward-mode"):
+                call()
+        with torch.no_grad(), pytest.raises(NotImplementedError, match="forward-mode"):
+            window_attention(dual, x, x)
+    for call in (lambda t: window_attention(t, t, t), lambda t: rope.apply(t, pos)):
+        for t in (x, x.clone().requires_grad_()):
+            with pytest.raises(NotImplementedError, match="trace"):
+                torch.jit.trace(call, (t,))
+    with pytest.raises(ValueError):     # not refused for either: on the CPU
+        window_attention(x, x, x)
