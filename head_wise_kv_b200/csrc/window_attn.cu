@@ -19,8 +19,17 @@
 // softmax statistics, sums and D are fp32
 // (D from the result before its rounding, as far as 8 more bits hold it).  p_ij and ds_ij are rounded to the
 // inputs' type because a tcgen05 product needs both operands in one 16-bit
-// type: relative 2^-9 per element, averaged over the sums, the size of the
-// rounding of the result.
+// type: at most 2^-8 (bf16) or 2^-11 (fp16) of each element, averaged over the
+// sums, the size of the rounding of the result.
+//
+// fp16 is that exact from 2^-14 to 65504 only, and weights of long rows and
+// gradients lie anywhere.  There they are held times powers of two, which the
+// results take out again: the forward's weights 2^7 (below 2^15, the running
+// maximum may lag by 2^8), the backward's 2^14 (at most 1 before), ds a factor
+// f of each (sequence, key head).  |g_i.v_j - D_i| p_ij =
+// p (1 - p) |g_i.(v_j - the other keys' mean)| <= M / 2 with M = max |g_i| max |v_j|, so f
+// is the power of two that brings M into 2^14 .. 2^15.  What then falls below
+// 2^-14 is off by at most 2^-32 of the row's largest weight, 2^-39, and 2^-39 M.
 //
 // No atomics: the backward visits each tile pair twice, once for the key
 // tile's owner (dK, dV) and once for the query tile's (dQ).  That is 7
@@ -55,9 +64,11 @@ constexpr float kRescaleThreshold = 8.0f;     // log2 units
 
 template <typename T>
 struct Elem;
+constexpr int kWeightShift = 14;              // fp16: log2 of the factor of the backward's weights
 template <>
 struct Elem<__nv_bfloat16> {
     static constexpr bool bf16 = true;
+    static constexpr float kForwardShift = 0.f, kStatsShift = 0.f;
     static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
         const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
         return *reinterpret_cast<const uint32_t*>(&h);
@@ -67,6 +78,7 @@ struct Elem<__nv_bfloat16> {
 template <>
 struct Elem<__half> {
     static constexpr bool bf16 = false;
+    static constexpr float kForwardShift = 7.f, kStatsShift = float(kWeightShift);   // log2 of the weights' factors
     static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
         const __half2 h = __floats2half2_rn(lo, hi);
         return *reinterpret_cast<const uint32_t*>(&h);
@@ -242,6 +254,7 @@ struct Bars {
     uint64_t s_full[2], s_read, dp_full, dp_read, p_half[2], p_full[2], ds_full[2], trimmed, done[2], fin;
     uint32_t tmem;
     int abort_flag;
+    float peak[2][8];
 };
 constexpr uint32_t kSmem = kBarsAt + sizeof(Bars);
 static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
@@ -543,7 +556,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
                 }
             }
             float2 acc[4] = {};
-            const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nm2 = make_float2(-m, -m);
+            const float nm = Elem<T>::kForwardShift - m;
+            const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nm2 = make_float2(nm, nm);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 uint32_t ph[16];
@@ -583,7 +597,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
             tc_fence_after();
             const bool row = i < len;
             const float inv = row && l > 0.f ? 1.f / l : 0.f;
-            p.stats[row0 + i] = row && l > 0.f ? -(m + __log2f(l)) : -CUDART_INF_F;
+            p.stats[row0 + i] =
+                row && l > 0.f ? Elem<T>::kForwardShift + Elem<T>::kStatsShift - (m + __log2f(l)) : -CUDART_INF_F;
             // through this tile's Q, which no product reads any more
             const uint32_t tile = sQ + x * kTileBytes;
             uint4* low = reinterpret_cast<uint4*>(p.low + (row0 + qt * kTile) * kTile) + r;
@@ -626,15 +641,62 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
 // once; writes minus D.  The remainder matters where few keys share a row:
 // the rounding of o_i is then as large beside D_i as that of ds.  Sixteen
 // threads per row, four rows per thread.  Measured: 17 us for 84 MB from cold
-// caches (32 heads x 4096 tokens), 0.75 of the copy rate.
+// caches (32 heads x 4096 tokens), 0.75 of the copy rate.  In fp16 each block
+// also leaves the largest |g_i|^2 of its rows, and blocks behind these that of
+// the values' rows: what ds is scaled by.
 constexpr int kDeltaRows = 4;
+
+// The largest of 256 threads' numbers (not below zero), by one of them.
+__device__ __forceinline__ void store_largest(float x, float* to) {
+    __shared__ float top[8];
+    const float w = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(x)));
+    if (threadIdx.x % 32 == 0) top[threadIdx.x / 32] = w;
+    __syncthreads();
+    if (threadIdx.x == 0)
+        *to = fmaxf(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), fmaxf(fmaxf(top[4], top[5]), fmaxf(top[6], top[7])));
+}
+
+// The sum of 8 elements' squares.
+template <typename T>
+__device__ __forceinline__ float squares(const uint4& x) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    float s = 0.f;
+#pragma unroll
+    for (int z = 0; z < 4; ++z) {
+        const float2 u = Elem<T>::wide(w[z]);
+        s = fmaf(u.x, u.x, fmaf(u.y, u.y, s));
+    }
+    return s;
+}
+
+// Of 16 threads' numbers that make up a row.
+__device__ __forceinline__ float row_sum(float d) {
+#pragma unroll
+    for (int z = 8; z > 0; z >>= 1) d += __shfl_xor_sync(0xffffffffu, d, z);
+    return d;
+}
 
 template <typename T>
 __global__ void __launch_bounds__(256) window_delta_kernel(const __grid_constant__ WindowAttnParams p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     // blockIdx.x: 64 rows of a (sequence, head); Tp is a multiple of 64
-    const int blocks = p.Tp / (16 * kDeltaRows), bh = int(blockIdx.x) / blocks, b = bh / p.hq, h = bh - b * p.hq;
+    const int blocks = p.Tp / (16 * kDeltaRows);
+    if (!Elem<T>::bf16 && int(blockIdx.x) >= blocks * p.B * p.hq) {       // 64 rows of the values
+        const int bg = int(blockIdx.x) / blocks - p.B * p.hq, b = bg / p.n_kv, len = length_of(p, b);
+        const int t0 = int(blockIdx.x) % blocks * (16 * kDeltaRows) + threadIdx.x / 16;
+        float top = 0.f;
+#pragma unroll
+        for (int k = 0; k < kDeltaRows; ++k) {
+            const int t = t0 + 16 * k;
+            uint4 x = make_uint4(0, 0, 0, 0);
+            if (t < len) x = *reinterpret_cast<const uint4*>(row_at<const T>(p.v, b, bg - b * p.n_kv, t) + threadIdx.x % 16 * 8);
+            top = fmaxf(top, row_sum(squares<T>(x)));
+        }
+        store_largest(top, p.peak + blockIdx.x);
+        return;
+    }
+    const int bh = int(blockIdx.x) / blocks, b = bh / p.hq, h = bh - b * p.hq;
     const int t0 = (int(blockIdx.x) - bh * blocks) * (16 * kDeltaRows) + threadIdx.x / 16, part = threadIdx.x % 16;
     const int len = length_of(p, b);
     uint4 x[kDeltaRows], y[kDeltaRows];
@@ -651,6 +713,7 @@ __global__ void __launch_bounds__(256) window_delta_kernel(const __grid_constant
                                                        (part / 2 * kTile + t % kTile) * 16 + part % 2 * 8);
         }
     }
+    float top = 0.f;
 #pragma unroll
     for (int k = 0; k < kDeltaRows; ++k) {
         const uint32_t xs[4] = {x[k].x, x[k].y, x[k].z, x[k].w}, ys[4] = {y[k].x, y[k].y, y[k].z, y[k].w};
@@ -664,11 +727,11 @@ __global__ void __launch_bounds__(256) window_delta_kernel(const __grid_constant
             d = fmaf(u.x, v.x, fmaf(u.y, v.y, d));
             rest = fmaf(w.x, v.x, fmaf(w.y, v.y, rest));
         }
-        d = fmaf(rest, 1.f / kLowScale, d);
-#pragma unroll
-        for (int z = 8; z > 0; z >>= 1) d += __shfl_xor_sync(0xffffffffu, d, z);
+        d = row_sum(fmaf(rest, 1.f / kLowScale, d));
         if (part == 0) p.delta[int64_t(bh) * p.Tp + t0 + 16 * k] = -d;
+        if (!Elem<T>::bf16) top = fmaxf(top, row_sum(squares<T>(y[k])));
     }
+    if (!Elem<T>::bf16) store_largest(top, p.peak + blockIdx.x);
 }
 
 // ------------------------------------------------------------------ backward
@@ -703,6 +766,35 @@ struct KeyItem {
         x1 = int(all * (piece + 1) / pieces);
     }
 };
+
+// fp16: h with M in 2^h .. 2^(h + 1) for a sequence's key head; ds is held times f = 2^(kWeightShift - h), by
+// warps 0 .. 7 together.  Without a gradient, or with one that is not finite, f = 1.  bf16: ds as it is.
+template <typename T>
+__device__ __forceinline__ int ds_exponent(const WindowAttnParams& p, Bars& sh, int b, int g) {
+    if (Elem<T>::bf16) return 0;
+    const int blocks = p.Tp / (16 * kDeltaRows);
+    const float *pg = p.peak + (int64_t(b) * p.hq + g * p.G) * blocks,
+                *pv = p.peak + (int64_t(p.B) * p.hq + int64_t(b) * p.n_kv + g) * blocks;
+    float x = 0.f, y = 0.f;
+    for (int i = threadIdx.x; i < p.G * blocks; i += 256) x = fmaxf(x, pg[i]);
+    for (int i = threadIdx.x; i < blocks; i += 256) y = fmaxf(y, pv[i]);
+    x = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(x)));
+    y = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(y)));
+    if (threadIdx.x % 32 == 0) {
+        sh.peak[0][threadIdx.x / 32] = x;
+        sh.peak[1][threadIdx.x / 32] = y;
+    }
+    named_bar_sync(1, 256);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        x = fmaxf(x, sh.peak[0][i]);
+        y = fmaxf(y, sh.peak[1][i]);
+    }
+    const float m2 = x * y;             // M^2: below 2^79, and above 2^-97 where it is not zero
+    return m2 > 0.f && m2 < CUDART_INF_F ? (int(__float_as_uint(m2) >> 23) - 127) >> 1 : kWeightShift;
+}
+
+__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(uint32_t(e + 127) << 23); }
 
 // Key tile: K, V stay; Q (a ring of three) and g (of two) pass.  With keys
 // along the TMEM lanes,
@@ -819,6 +911,8 @@ __device__ __forceinline__ void key_tile(const WindowAttnParams& p, Bars& sh, ui
             if (qt == end_tile) ok = trim(&sh.full3[0], sQ, 0, 0);
             if (ok) arrive_warp(&sh.dp_read);
         }
+        const int h = ds_exponent<T>(p, sh, it.b, it.g);
+        const float2 f2 = make_float2(power_of_two(-h), power_of_two(-h));     // the weights carry 2^kWeightShift
         // dS of step x, once that of the step before has been used
         const auto put_ds = [&](int x) {
             if (x > 0 && !wait.warp(smem_addr(&sh.empty3[(x - 1) % kRing3]), ((x - 1) / kRing3) & 1)) return false;
@@ -898,7 +992,11 @@ __device__ __forceinline__ void key_tile(const WindowAttnParams& p, Bars& sh, ui
 #pragma unroll
             for (int c = 0; c < 64; c += 4) {
                 const uint4 dl = lds128(delta + c * 4);
-                const float* e = s + c;
+                float* e = s + c;
+                if (!Elem<T>::bf16) {
+                    *reinterpret_cast<float2*>(e) = fmul2(make_float2(e[0], e[1]), f2);
+                    *reinterpret_cast<float2*>(e + 2) = fmul2(make_float2(e[2], e[3]), f2);
+                }
                 const float2 y = fmul2(make_float2(e[0], e[1]),
                                        fadd2(make_float2(__uint_as_float(d[c]), __uint_as_float(d[c + 1])),
                                              make_float2(__uint_as_float(dl.x), __uint_as_float(dl.y))));
@@ -913,6 +1011,9 @@ __device__ __forceinline__ void key_tile(const WindowAttnParams& p, Bars& sh, ui
         if (all_agree(1, 256, ok && wait.warp(smem_addr(&sh.done[0]), 0))) {
             tc_fence_after();
             const bool row = key < len && n > 0;
+            // what the sums were held times, taken out
+            const float held[2] = {Elem<T>::bf16 ? 1.f : power_of_two(h - kWeightShift),
+                                   Elem<T>::bf16 ? 1.f : power_of_two(-kWeightShift)};
             // through the ring: all products that read it are done
             const uint32_t tile[2] = {sQ, sQ + kTileBytes};
 #pragma unroll
@@ -927,14 +1028,15 @@ __device__ __forceinline__ void key_tile(const WindowAttnParams& p, Bars& sh, ui
                                     (cb + c * 32) / 4 * kTile + r;
 #pragma unroll
                         for (int z = 0; z < 32; z += 4)
-                            y[z / 4 * kTile] = row ? make_float4(__uint_as_float(o[z]), __uint_as_float(o[z + 1]),
-                                                                 __uint_as_float(o[z + 2]), __uint_as_float(o[z + 3]))
+                            y[z / 4 * kTile] = row ? make_float4(__uint_as_float(o[z]) * held[w], __uint_as_float(o[z + 1]) * held[w],
+                                                                 __uint_as_float(o[z + 2]) * held[w],
+                                                                 __uint_as_float(o[z + 3]) * held[w])
                                                    : make_float4(0.f, 0.f, 0.f, 0.f);
                     } else {
                         uint4 v[4];
 #pragma unroll
                         for (int z = 0; z < 4; ++z)
-                            v[z] = row ? pack8<T>(o + 8 * z, w ? 1.f : p.scale) : make_uint4(0, 0, 0, 0);
+                            v[z] = row ? pack8<T>(o + 8 * z, (w ? 1.f : p.scale) * held[w]) : make_uint4(0, 0, 0, 0);
                         put_row(tile[w], r, cb + c * 32, v);
                     }
                 }
@@ -1038,7 +1140,9 @@ __device__ __forceinline__ void query_tile(const WindowAttnParams& p, Bars& sh, 
         const int quarter = warp & 3, half = warp >> 2, r = quarter * 32 + lane, i = i0 + r, cb = half * 64;
         const uint32_t at = tmem + (uint32_t(quarter * 32) << 16) + cb;
         const int64_t row = (int64_t(b) * p.hq + h) * p.Tp + i;
-        const float nl = p.stats[row], dl = p.delta[row];
+        const int e = ds_exponent<T>(p, sh, b, g);      // p_ij f = 2^(s + nl): the factor costs nothing here
+        const float nl = p.stats[row] - (Elem<T>::bf16 ? 0.f : float(e)), dl = p.delta[row];
+        const float scale = Elem<T>::bf16 ? p.scale : p.scale * power_of_two(e - kWeightShift);
         const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nl2 = make_float2(nl, nl), dl2 = make_float2(dl, dl);
         // where the sequence ends inside the last key tile, what lies behind becomes
         // zeros before any product, a step ahead
@@ -1109,7 +1213,7 @@ __device__ __forceinline__ void query_tile(const WindowAttnParams& p, Bars& sh, 
                 tmem_ld32(at + kDQ + c * 32, o);
                 tmem_wait_ld();
 #pragma unroll
-                for (int z = 0; z < 4; ++z) v[z] = i < len ? pack8<T>(o + 8 * z, p.scale) : make_uint4(0, 0, 0, 0);
+                for (int z = 0; z < 4; ++z) v[z] = i < len ? pack8<T>(o + 8 * z, scale) : make_uint4(0, 0, 0, 0);
                 put_row(sK, r, cb + c * 32, v);
             }
             fence_proxy_async_smem();
@@ -1286,6 +1390,11 @@ void plan_pairs(WindowAttnParams& p, int num_sms) {
     p.pairs = 2 * rest <= num_sms ? all - rest : all;
 }
 
+// Floats of `peak`.
+int64_t peaks(const WindowAttnParams& p, int dtype) {
+    return dtype == DUO_BF16 ? 0 : int64_t(p.B) * (p.hq + p.n_kv) * (p.Tp / (16 * kDeltaRows));
+}
+
 int64_t partial_slots(const WindowAttnParams& p) {
     const int64_t bk = int64_t(p.B) * p.n_kv;
     return (p.p_long > 1 ? int64_t(p.n_long) * p.p_long * bk : 0) +
@@ -1332,7 +1441,7 @@ int run_forward(const WindowAttnParams& p, cudaStream_t s) {
 
 template <typename T>
 int run_backward(const WindowAttnParams& p, cudaStream_t s) {
-    const unsigned rows = unsigned(p.B) * p.hq * (p.Tp / (16 * kDeltaRows));
+    const unsigned rows = unsigned(p.B) * (p.hq + (Elem<T>::bf16 ? 0 : p.n_kv)) * (p.Tp / (16 * kDeltaRows));
     if (launch(window_delta_kernel<T>, p, dim3(rows), 256, 0, s) != cudaSuccess) return DUO_ERR_CUDA;
     const unsigned items = unsigned(p.items_kv + p.n_t * p.B * p.hq);
     if (launch(window_bwd_kernel<T>, p, dim3(items), kThreads, kSmem, s) != cudaSuccess) return DUO_ERR_CUDA;
@@ -1366,7 +1475,7 @@ int duo_window_attn_workspace_bytes(const duo_window_attn_desc* d, size_t* bytes
     duo::fill_params(p, *d, nullptr, nullptr);
     duo::plan_pieces(p, sms);
     *bytes = duo::align256(size_t(d->batch) * d->num_q_heads * p.Tp * 4) +
-             size_t(duo::partial_slots(p)) * 2 * duo::kTile * duo::kTile * 4;
+             duo::align256(size_t(duo::peaks(p, d->dtype)) * 4) + size_t(duo::partial_slots(p)) * 2 * duo::kTile * duo::kTile * 4;
     return DUO_OK;
 }
 
@@ -1419,13 +1528,15 @@ int duo_window_attn_grad(const duo_window_attn_desc* d, const duo_heads* q, cons
         !duo::make_map(&p.tm_dq, *dq, *d, p.hq) || !duo::make_map(&p.tm_dk, *dk, *d, p.n_kv) ||
         !duo::make_map(&p.tm_dv, *dv, *d, p.n_kv))
         return DUO_ERR_CUDA;
+    p.v = duo::head_tensor(*v);
     p.out = duo::head_tensor(*out);
     p.dout = duo::head_tensor(*dout);
     p.dk = duo::head_tensor(*dk);
     p.dv = duo::head_tensor(*dv);
     p.delta = static_cast<float*>(workspace);
-    p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) +
-                                      duo::align256(size_t(p.B) * p.hq * p.Tp * 4));
+    p.peak = reinterpret_cast<float*>(static_cast<char*>(workspace) + duo::align256(size_t(p.B) * p.hq * p.Tp * 4));
+    p.part = reinterpret_cast<float*>(reinterpret_cast<char*>(p.peak) +
+                                      duo::align256(size_t(duo::peaks(p, d->dtype)) * 4));
     return d->dtype == DUO_BF16 ? duo::run_backward<__nv_bfloat16>(p, stream) : duo::run_backward<__half>(p, stream);
 }
 

@@ -700,7 +700,11 @@ DUO_API int duo_window_attn_workspace_bytes(const duo_window_attn_desc* desc, si
 /* out = softmax(scale q k^T) v over the visible keys: the two branches of
  * the gated forward that tells retrieval heads (window = 0) from streaming
  * ones.  Products in the inputs' type with fp32 sums, softmax in fp32, one
- * rounding of the result.
+ * rounding of the result.  Weights (and in the gradient weights times their
+ * own gradients) are rounded to the inputs' type; in fp16 they are held times
+ * powers of two, so that neither long rows nor small or large gradients leave
+ * its range.  Scaled scores, scale |q_i.k_j|, stay below 2^23: a weight of the
+ * gradient is off by about 2^-24 of itself times them.
  *   stats: device, duo_window_attn_stats_bytes, 16-byte aligned;
  *   status: device int32 word or NULL: a pipeline wait that ran out sets
  *     DUO_STATUS_WAIT_TIMEOUT there (the result then means nothing).

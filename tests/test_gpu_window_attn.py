@@ -406,3 +406,124 @@ def test_garbage_behind_sequences_of_many_heads(B, hq, n_kv, T, sink, window):
         for b, n in enumerate(lengths):
             x[b, :, n:] = float("nan")
     assert all(torch.equal(a, b) for a, b in zip(clean, _run(q, k, v, g, sink, window, lengths)))
+
+
+# fp16 holds 11 bits from 2^-14 to 65504 only.  Weights and ds are held times powers of two, so beside half a step of
+# each (u = 2^-11) there remain, absolute: 2^-32 of the row's largest weight in the forward (2^-25, the weights held
+# times 2^7, and the running maximum never above the last), 2^-39 of a weight in the backward (2^-25, times 2^14), and
+# 2^-39 M of ds with M = max |g_i| max |v_j| over the heads that share a key head (2^-25 / f, f >= 2^14 / M).  The
+# result's own rounding has a smallest half step of 2^-25.
+def _reference_fp16(q, k, v, g, sees, scale, M):
+    u = 2.0 ** -11
+    out, p = O.window_attention(q, k, v, sees, scale)
+    dq, dk, dv = O.window_attention_grad(q, k, v, g, sees, scale)
+    aq, ak, av, ag = (np.abs(x) for x in (q, k, v, g))
+    ep = 2 * scale * 2.0 ** -16 * float((aq @ ak.T).max()) + 2.0 ** -18
+    seen = sees.astype(np.float64)
+    step = 2.0 ** -25
+    top = p.max(1, keepdims=True)
+    eo = (u + ep) * (p @ av) + 2.0 ** -32 * top * (seen @ av) + u * np.abs(out) + step
+    ev = (u + ep) * (p.T @ ag) + 2.0 ** -39 * (seen.T @ ag) + u * np.abs(dv) + step
+    ds = p * (g @ v.T - (g * out).sum(1, keepdims=True))
+    es = p * (2.0 ** -16 * (ag @ av.T) + (ag * eo).sum(1, keepdims=True)) + (u + ep + 2.0 ** -16) * np.abs(ds) + \
+        2.0 ** -39 * M * seen
+    eq = scale * es @ ak + u * np.abs(dq) + step
+    ek = scale * es.T @ aq + u * np.abs(dk) + step
+    return (out, dq, dk, dv), (eo, eq, ek, ev)
+
+
+def _within_fp16(name, y, ref, bound):
+    """A result from 65520 on rounds to infinity in fp16, and only such a one may."""
+    big = np.abs(ref) - bound >= 65520
+    assert np.array_equal(y[big], np.sign(ref[big]) * np.inf), name
+    may = np.isinf(y) & (np.abs(ref) + bound >= 65520) & (np.sign(y) == np.sign(ref))
+    _within(name, np.where(big | may, ref, y), ref, bound, len(y))
+
+
+def _check_fp16(x, got, sink, window):
+    q, k, v, g = (t.detach().double().cpu().numpy()[0] for t in x)
+    res = [t.detach().double().cpu().numpy()[0] for t in got]
+    T, G = q.shape[1], len(q) // len(k)
+    sees = O.window_visible(T, sink, window or 0)
+    for kv in range(len(k)):
+        group = range(kv * G, kv * G + G)
+        M = max(np.linalg.norm(g[h], axis=1).max() for h in group) * np.linalg.norm(v[kv], axis=1).max()
+        refs = [_reference_fp16(q[h], k[kv], v[kv], g[h], sees, 128 ** -0.5, M) for h in group]
+        for h, (ref, bound) in zip(group, refs):
+            _within_fp16(f"out h{h}", res[0][h], ref[0], bound[0])
+            _within_fp16(f"dq h{h}", res[1][h], ref[1], bound[1])
+        for i, name in ((2, "dk"), (3, "dv")):
+            _within_fp16(f"{name} kv{kv}", res[i][kv], sum(r[0][i] for r in refs), sum(r[1][i] for r in refs))
+
+
+@pytest.mark.parametrize("T,size,sink,window", [(900, 2.0 ** -22, 0, None), (2300, 2.0 ** -20, 0, None), (700, 2.0 ** -24, 70, 300),
+                                                (130, 2.0 ** -8, 0, None), (60, 512.0, 0, None), (200, 4096.0, 3, 50)])
+@pytest.mark.parametrize("hq,n_kv", [(2, 1), (2, 2)])
+def test_fp16_gradients_of_any_size(T, size, sink, window, hq, n_kv):
+    """ds from far below fp16's smallest step to above its largest value, all of a key's with one sign.
+
+    Values are plus or minus one pattern, gradients the pattern times `size`, so g.v = +- 128 size |v|.  Keys hold the
+    value's sign in a dimension that queries leave out and queries a one in another that keys leave out: sums over ds
+    add up to gradients of a size that fp16 holds."""
+    gen = torch.Generator().manual_seed(T)
+    pattern = torch.where(torch.rand(128, generator=gen) < 0.5, -1.0, 1.0)
+    sign = torch.where(torch.rand(n_kv, T, 1, generator=gen) < 0.5, -1.0, 1.0)
+    large = size >= 1           # then small queries and keys, and rows of either sign: what comes out has to fit
+    v_size, other = (64.0, 2.0 ** -6 * 512 / size) if large else (1.0, 1.0)
+    unit = other / 4 if large else (8.0 if size < 2.0 ** -15 else 1.0)
+    q = other * torch.randn(1, hq, T, 128, generator=gen)
+    k = other * torch.randn(1, n_kv, T, 128, generator=gen)
+    q[..., 0], k[..., 1] = 0, 0
+    q[..., 1], k[..., 0] = unit, unit * sign[..., 0]
+    v = (v_size * pattern * sign)[None]
+    g = size * (pattern * (1 + torch.arange(hq)[:, None, None] % 2)).expand(1, hq, T, 128)
+    if large:
+        g = g * torch.where(torch.rand(1, hq, T, 1, generator=gen) < 0.5, -1.0, 1.0)
+    x = [t.to(torch.float16).to(DEV) for t in (q, k, v, g)]
+    got = _run(*x, sink, window)
+    assert float(got[1][..., T // 2:, 0].abs().min()) > 0 and float(got[2][..., 1].abs().max()) > 0
+    _check_fp16(x, got, sink, window)
+
+
+@pytest.mark.parametrize("T,gap", [(1500, 20), (1500, 26), (300, 30)])
+def test_fp16_weights_far_below_the_largest(T, gap):
+    """One key of weight nearly 1, the others 2^-gap of it each: their share of out and their dv."""
+    gen = torch.Generator().manual_seed(gap)
+    q, k, v, g = (torch.zeros(1, 1, T, 128) for _ in range(4))
+    q[..., 0], k[0, 0, 0, 0] = 16.0, gap * 0.6931471805599453 * 128 ** 0.5 / 16
+    v[..., 1:] = 64 * torch.rand(1, 1, T, 127, generator=gen)
+    v[0, 0, 0] = 0
+    g[:] = 64 * torch.rand(1, 1, T, 128, generator=gen)
+    x = [t.to(torch.float16).to(DEV) for t in (q, k, v, g)]
+    got = _run(*x, 0, None)
+    # 1500 rows, gap 20: D_i = g.out is about 127 x 32 x 32 x 2^-20 i = 0.12 i, and dk of the first key
+    # -16 x 128^-0.5 x (the sum of D_i: 1.4e5) = -2e5, which fp16 holds as -inf
+    _check_fp16(x, got, 0, None)
+    assert float(got[3][0, 0, 1, 5].abs()) > 0
+
+
+def test_fp16_rows_of_very_different_gradients():
+    """Most of a sequence gets no gradient or a small one, and each head its own scale."""
+    q, k, v, g = _make(1, 4, 2, 600, torch.float16, False, 31)
+    size = torch.exp2(-torch.randint(0, 24, (1, 4, 600, 1), generator=torch.Generator().manual_seed(1)).float()).to(DEV)
+    size[:, :, ::7] = 0
+    g = (g * size).to(torch.float16)
+    x = [q, k, v, g]
+    _check_fp16(x, _run(*x, 16, 200), 16, 200)
+    zero = torch.zeros_like(g)
+    assert not any(t.any() for t in _run(q, k, v, zero, 16, 200)[1:])
+
+
+def test_fp16_gradient_captured_and_replayed():
+    """The factor of ds is that of each replay's gradients."""
+    from head_wise_kv_b200 import window_attention
+    q, k, v, g = _make(1, 4, 2, 300, torch.float16, True, 32)
+    x = [t.detach().clone().requires_grad_() for t in (q, k, v)]
+    gg = g.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        res = torch.autograd.grad(window_attention(*x, 8, 60), x, gg)
+    for size in (2.0 ** -20, 256.0, 2.0 ** -12):
+        gg.copy_(g * size)
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(res, _run(q, k, v, gg, 8, 60)[1:]))
