@@ -500,3 +500,24 @@ def test_tangents_are_refused():
                 with pytest.raises(NotImplementedError, match="forward-mode"):
                     call()
     assert torch.equal(c.buf, before)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("strided", [False, True])
+def test_prefill_rope_caches_what_append_rope_does(kind, strided):
+    """The same token has the same codes whichever call it came by: quantised from the fp32 rotated value."""
+    st = Setup(kind, cap=800)
+    scale = st.d ** -0.5
+    lens = torch.zeros(3, dtype=torch.int32, device=DEV)
+    for C, counts in ((130, [130, 1, 77]), (1, [1, 1, 1]), (60, [33, 60, 2])):
+        q, k, v = _qkv(st, 0, C, (3, C + (5 if strided else 0)))
+        if strided:         # a part of a longer batch: sequences do not follow one another at the token stride
+            q, k, v = (t[:, 3:3 + C] for t in (q, k, v))
+        n = None if len(set(counts)) == 1 and counts[0] == C else torch.tensor(counts, dtype=torch.int32, device=DEV)
+        st.caches[0].prefill_rope(0, st.rope, q, k, v, lens, scale, n_new=n)
+        st.caches[1].append_rope(0, st.rope, None, k.contiguous(), v.contiguous(), lens, n_new=n)
+        a, b = (c.layer_views(0) for c in st.caches)
+        for name in ("k_retrieval", "v_retrieval", "k_streaming", "v_streaming", "positions"):
+            assert _same(a[name], b[name]), name
+        lens = lens + torch.tensor(counts, dtype=torch.int32, device=DEV)
+    assert st.caches[0].status() == st.caches[1].status() == 0
