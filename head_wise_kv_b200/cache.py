@@ -351,8 +351,11 @@ class DuoKVCache:
             if t.device != self.device:
                 raise ValueError(f"{name}: on {t.device}, expected {self.device}")
             src.append(t.transpose(1, 2))
-        dst = [torch.empty(t.shape, dtype=torch.bfloat16, device=self.device) for t in src]
-        rope.launch([(src[0], dst[0], True), (src[1], dst[1], True), (src[2], dst[2], False)], prefix_len)
+        # keys and values behind a sequence's tokens are zeros, whatever the rows hold there: the last tokens share a
+        # tile with them, and a weight of zero times NaN is NaN
+        fill = torch.empty if n_new is None else torch.zeros
+        dst = [f(t.shape, dtype=torch.bfloat16, device=self.device) for f, t in zip((torch.empty, fill, fill), src)]
+        rope.launch([(src[0], dst[0], True), (src[1], dst[1], True), (src[2], dst[2], False)], prefix_len, n_new)
         with _on(self.device):
             out = self.prefill(layer, *dst, prefix_len, scale, out=out)
             if not (self.fp8 or self.int4):     # the rotated keys, rounded once as they are

@@ -521,3 +521,24 @@ def test_prefill_rope_caches_what_append_rope_does(kind, strided):
             assert _same(a[name], b[name]), name
         lens = lens + torch.tensor(counts, dtype=torch.int32, device=DEV)
     assert st.caches[0].status() == st.caches[1].status() == 0
+
+
+@pytest.mark.parametrize("kind", ["bf16", "paged_fp8", "int4"])
+def test_prefill_rope_of_a_padded_batch_with_anything_in_its_padding(kind):
+    st = Setup(kind, cap=800)
+    lens = torch.zeros(3, dtype=torch.int32, device=DEV)
+    for C, counts in ((150, [150, 90, 0]), (70, [1, 70, 63])):
+        n = torch.tensor(counts, dtype=torch.int32, device=DEV)
+        clean = [t.contiguous() for t in _qkv(st, 0, C, (3, C))]
+        want = st.caches[0].prefill_rope(0, st.rope, *clean, lens, st.d ** -0.5, n_new=n)
+        bad = [t.clone() for t in clean]
+        for t, x in zip(bad, (float("nan"), float("inf"), float("nan"))):
+            for b, c in enumerate(counts):
+                t[b, c:] = x
+        bad[2][0, counts[0] + 3:] = 3e38
+        got = st.caches[1].prefill_rope(0, st.rope, *bad, lens, st.d ** -0.5, n_new=n)
+        for b, c in enumerate(counts):
+            assert torch.isfinite(want[b, :, :c]).all() and torch.equal(want[b, :, :c], got[b, :, :c]), (C, b)
+        assert torch.equal(st.caches[0].buf, st.caches[1].buf)
+        lens = lens + n
+    assert st.caches[0].status() == st.caches[1].status() == 0
