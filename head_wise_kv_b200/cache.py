@@ -337,8 +337,9 @@ class DuoKVCache:
         heads): rotate at positions prefix_len + i and lay out head-major (one
         launch), attend (``prefill``), then append the chunk, of which
         sequence b has its first n_new[b] tokens (int32 [B], default C); what
-        the cache holds is what ``append_rope`` writes.  Returns fp32 out [B][Hq][C][d]; rows at and behind n_new[b] mean
-        nothing."""
+        the cache holds is what ``append_rope`` writes.  Returns fp32 out
+        [B][Hq][C][d]; rows at and behind n_new[b] mean nothing, and what q, k
+        and v hold there does not matter."""
         if rope.d != self.d:
             raise ValueError(f"rope of head_dim {rope.d}, expected {self.d}")
         C = q.shape[1]

@@ -279,9 +279,10 @@ int duo_kv_append_rope(duo_kv* kv, int32_t layer, const duo_rope* rope, const du
                        const duo_rows* v, const int32_t* len_before, const duo_token_map* map, const int32_t* n_new,
                        int32_t n_tokens, uint16_t* q_out, duo_stream_t stream) {
     if (!kv || layer < 0 || layer >= kv->desc.num_layers || !rope || n_tokens < 0) return DUO_ERR_INVALID_ARG;
-    if (rope->desc.head_dim != kv->desc.head_dim || (q != nullptr) != (q_out != nullptr)) return DUO_ERR_INVALID_ARG;
-    if (map && (n_new || !map->seq || !map->pos || !map->len_after)) return DUO_ERR_INVALID_ARG;
-    if (n_tokens == 0) return DUO_OK;
+    if (rope->desc.head_dim != kv->desc.head_dim) return DUO_ERR_INVALID_ARG;
+    if (map && (n_new || !map->len_after)) return DUO_ERR_INVALID_ARG;
+    if (n_tokens == 0) return DUO_OK;      // arrays of no entries may be NULL
+    if ((q != nullptr) != (q_out != nullptr) || (map && (!map->seq || !map->pos))) return DUO_ERR_INVALID_ARG;
     if (!len_before) return DUO_ERR_INVALID_ARG;
     for (const duo_rows* r : {q, k, v}) {
         if (r == q && !q) continue;

@@ -542,3 +542,23 @@ def test_prefill_rope_of_a_padded_batch_with_anything_in_its_padding(kind):
         assert torch.equal(st.caches[0].buf, st.caches[1].buf)
         lens = lens + n
     assert st.caches[0].status() == st.caches[1].status() == 0
+
+
+def test_a_step_without_tokens():
+    """A map of no entries, and a padded batch of none: nothing is written, and the rotated queries are empty."""
+    from head_wise_kv_b200 import TokenMap
+    st = Setup("bf16", caches=1)
+    c = st.caches[0]
+    before = c.buf.clone()
+    zero = torch.zeros(3, dtype=torch.int32, device=DEV)
+    q, k, v = _qkv(st, 0, 1)
+    m = TokenMap(3, 0, DEV)
+    c.reserve(zero, zero, m)
+    assert m.cu.tolist() == [0] * 4
+    for out in (None, torch.empty(0, st.hq, st.d, dtype=torch.bfloat16, device=DEV)):
+        assert c.append_rope(0, st.rope, q, k, v, zero, m, out=out).shape == (0, st.hq, st.d)
+    assert c.append_rope(0, st.rope, None, k, v, zero, m) is None
+    q, k, v = _qkv(st, 0, 1, (3, 0))
+    assert c.append_rope(0, st.rope, q, k, v, zero).shape == (3, 0, st.hq, st.d)
+    assert c.append_rope(0, st.rope, q, k, v, zero, n_new=zero).shape == (3, 0, st.hq, st.d)
+    assert torch.equal(c.buf, before) and c.status() == 0
