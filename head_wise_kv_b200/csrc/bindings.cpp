@@ -6,6 +6,7 @@
 // attention's forward and backward).  Nothing is computed here: every step of
 // the path runs in the library's kernels (duo_kv.h).
 #include <ATen/core/grad_mode.h>
+#include <c10/core/InferenceMode.h>
 #include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -489,6 +490,7 @@ Tensor status_word(const at::Device& dev) {
         (void)cudaStreamDestroy(own);
         if (e != cudaSuccess && word) (void)cudaFree(word);
         C10_CUDA_CHECK(e);
+        const c10::InferenceMode off(false);      // it outlives the mode of its first call, and is cleared outside it
         (*words)[i] = at::from_blob(word, {1}, at::TensorOptions().dtype(at::kInt).device(dev));
     }
     return (*words)[i];

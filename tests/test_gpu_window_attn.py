@@ -527,3 +527,25 @@ def test_fp16_gradient_captured_and_replayed():
         gg.copy_(g * size)
         graph.replay()
         assert all(torch.equal(a, b) for a, b in zip(res, _run(q, k, v, gg, 8, 60)[1:]))
+
+
+_FIRST_IN_INFERENCE = """
+import torch
+from head_wise_kv_b200 import window_attention, window_attention_status
+x = [torch.randn(1, 2, 40, 128, device="cuda:0", dtype=torch.bfloat16) for _ in range(3)]
+with torch.inference_mode():
+    got = window_attention(*x, 2, 9)
+    assert window_attention_status("cuda:0") == 0
+assert window_attention_status("cuda:0") == 0
+y = [t.clone().requires_grad_() for t in x]
+out = window_attention(*y, 2, 9)
+out.sum().backward()
+assert torch.equal(got, out) and window_attention_status("cuda:0") == 0
+"""
+
+
+def test_status_outlives_the_inference_mode_of_the_first_call():
+    import subprocess
+    import sys
+    done = subprocess.run([sys.executable, "-c", _FIRST_IN_INFERENCE], capture_output=True, text=True, timeout=240)
+    assert done.returncode == 0, done.stderr[-2000:]
