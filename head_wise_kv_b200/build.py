@@ -1,5 +1,6 @@
 """Build libduo_kv.so in-tree for sm_100a with nvcc, and the compiled half of
-the Python binding (_binding.so) with g++ against torch's headers.
+the Python binding (_binding.so) with g++ against torch's headers.  Without
+torch only the library is built: a C program needs no more.
 
     python -m head_wise_kv_b200.build          # incremental
     python -m head_wise_kv_b200.build --force  # rebuild everything
@@ -7,6 +8,7 @@ the Python binding (_binding.so) with g++ against torch's headers.
 from __future__ import annotations
 
 import argparse
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -20,6 +22,7 @@ OBJDIR = os.path.join(ROOT, "_build", "duo_kv")
 LIB = os.path.join(PKG, "libduo_kv.so")
 BINDING_SRC = os.path.join(CSRC, "bindings.cpp")
 BINDING = os.path.join(PKG, "_binding.so")
+BUILT_FOR = os.path.join(OBJDIR, "_binding.built_for")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -65,15 +68,29 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
         if verbose:
             print(" ".join(cmd), flush=True)
         subprocess.run(cmd, check=True)
-    build_binding(force, verbose)
+    if importlib.util.find_spec("torch") is not None:
+        build_binding(force, verbose)
+    else:
+        print("head_wise_kv_b200: no torch, so no Python binding: built the C library alone", file=sys.stderr)
     return LIB
+
+
+def built_for() -> str:
+    """What _binding.so depends on besides its sources: the Python and torch that it was built against."""
+    import importlib.metadata
+    spec = importlib.util.find_spec("torch")
+    return f"python {sys.version}\ntorch {importlib.metadata.version('torch')} {spec.origin}\n"
 
 
 def build_binding(force: bool = False, verbose: bool = False) -> str:
     """_binding.so: links libduo_kv.so beside it and the torch that is installed."""
     inputs = [BINDING_SRC, os.path.join(INCLUDE, "duo_kv.h")]
+    stamp = built_for()
     if not force and os.path.exists(BINDING) and all(os.path.getmtime(BINDING) >= os.path.getmtime(f) for f in inputs):
-        return BINDING
+        if os.path.exists(BUILT_FOR):
+            with open(BUILT_FOR) as f:
+                if f.read() == stamp:
+                    return BINDING
     import sysconfig
 
     import torch
@@ -89,6 +106,9 @@ def build_binding(force: bool = False, verbose: bool = False) -> str:
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
+    os.makedirs(OBJDIR, exist_ok=True)
+    with open(BUILT_FOR, "w") as f:
+        f.write(stamp)
     return BINDING
 
 
