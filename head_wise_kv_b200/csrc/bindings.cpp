@@ -73,6 +73,12 @@ void check_plain(const Tensor& t, const char* name) {
                                 ": forward-mode derivatives are not implemented, the tangent would be lost");
 }
 
+// A tensor that a call has written, as in-place operations mark theirs: a backward pass that saved what was there
+// before then says so.
+void mark_written(const Tensor& t) {
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 void check_not_traced(const char* call) {
     TORCH_CHECK_NOT_IMPLEMENTED(!torch::jit::tracer::isTracing(), call, " cannot be traced: the trace would hold an empty result");
 }
@@ -287,6 +293,8 @@ Tensor rope_launch(uintptr_t plan, int64_t d, const RopeTask* tasks, size_t tens
     check(duo_rope_apply(reinterpret_cast<const duo_rope*>(plan), dtype, transpose, int32_t(B), int32_t(n), list,
                          int32_t(tensors), ints(positions), per_token, ints(n_new), stream_of(dev)),
           "duo_rope_apply");
+    for (size_t i = 0; i < tensors; ++i)
+        if (tasks[i].out) mark_written(*tasks[i].out);
     return first;
 }
 
@@ -392,6 +400,7 @@ struct Cache {
                                  ints(len_before), ragged ? &map : nullptr, ints(n_new), int32_t(lead.back()),
                                  out ? static_cast<uint16_t*>(out->data_ptr()) : nullptr, stream_of(dev)),
               "duo_kv_append_rope");
+        if (given) mark_written(*given);
         return out;
     }
 
@@ -425,6 +434,7 @@ struct Cache {
                              static_cast<int32_t*>(T ? pos.data_ptr() : none),
                              static_cast<int64_t*>(T ? slot.data_ptr() : none), stream_of(dev)),
               "duo_kv_reserve");
+        for (const Tensor* t : {&seq, &pos, &slot, &after, &cu}) mark_written(*t);
         return tokens;
     }
 
@@ -463,6 +473,8 @@ struct Cache {
                                    lse ? static_cast<float*>(lse->data_ptr()) : nullptr, ws.data_ptr(), ws.numel(),
                                    stream_of(dev)),
               "duo_decode_step_rope");
+        for (const OptTensor* t : given)
+            if (*t) mark_written(**t);
         if (lse) return py::make_tuple(out, *lse);
         return py::cast(out);
     }

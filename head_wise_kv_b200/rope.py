@@ -71,7 +71,7 @@ class Rope:
         where out is new).  transpose: the transposed map, i.e. the gradient.
         out may be x (in place).  Differentiable in x (backward mode) where
         out is not given."""
-        if x.requires_grad and torch.is_grad_enabled():
+        if torch.is_grad_enabled() and (x.requires_grad or out is not None and out.requires_grad):
             if out is not None:
                 raise ValueError("out cannot be given where a gradient is recorded")
             _b.check_recorded(x)

@@ -562,3 +562,44 @@ def test_a_step_without_tokens():
     assert c.append_rope(0, st.rope, q, k, v, zero).shape == (3, 0, st.hq, st.d)
     assert c.append_rope(0, st.rope, q, k, v, zero, n_new=zero).shape == (3, 0, st.hq, st.d)
     assert torch.equal(c.buf, before) and c.status() == 0
+
+
+def test_what_a_call_writes_counts_as_changed():
+    """A backward pass that saved a tensor which a call has since written refuses, as after any in-place operation."""
+    from head_wise_kv_b200 import Rope, TokenMap, window_attention
+    st = Setup("bf16", B=2, caches=1)
+    c, rope = st.caches[0], Rope(128)
+    zero, one = torch.zeros(2, dtype=torch.int32, device=DEV), torch.ones(2, dtype=torch.int32, device=DEV)
+    q, k, v = (t.contiguous() for t in _qkv(st, 2, 5))
+    m = TokenMap(2, 2, DEV)
+
+    def saved(t):
+        w = torch.ones_like(t).requires_grad_()
+        return w, (t * w).sum()
+    x = torch.randn(2, 3, 4, 128, device=DEV).to(torch.bfloat16)
+    out, lse, rot = torch.ones(2, 8, 128, device=DEV), torch.ones(2, 8, device=DEV), torch.ones_like(q)
+    for written, call in (((x,), lambda: rope.apply(x, zero, out=x)), ((x,), lambda: rope.launch([(x, x, True)], zero)),
+                          ((rot,), lambda: c.append_rope(0, st.rope, q[:, None], k[:, None], v[:, None], zero, out=rot[:, None])),
+                          ((out, lse, rot), lambda: c.step_rope(0, st.rope, q, k, v, zero, one, 0.1, out=out, lse=lse, q_rot=rot))):
+        graphs = [saved(t) for t in written]
+        with torch.no_grad():
+            call()
+        for w, loss in graphs:
+            with pytest.raises(RuntimeError, match="inplace"):
+                loss.backward()
+        w, loss = saved(written[0])     # and what is saved afterwards is good
+        loss.backward()
+        assert torch.equal(w.grad, written[0])
+    # lengths and positions that a later step moves on
+    x = [torch.randn(2, 2, 8, 128, device=DEV).to(torch.bfloat16).requires_grad_() for _ in range(3)]
+    c.reserve(zero, None, m)
+    att, y = window_attention(*x, lengths=m.len_after), rope.apply(x[0], m.len_after)
+    c.reserve(m.len_after, None, m)
+    for t in (att, y):
+        with pytest.raises(RuntimeError, match="inplace"):
+            t.sum().backward()
+    with torch.inference_mode():        # no versions there
+        t = torch.randn(2, 3, 4, 128, device=DEV).to(torch.bfloat16)
+        rope.apply(t, zero, out=t)
+    with pytest.raises(ValueError, match="recorded"):
+        rope.apply(x[0].detach(), zero, out=x[0])
