@@ -72,9 +72,10 @@ class Rope:
         out may be x (in place).  Differentiable in x (backward mode) where
         out is not given."""
         if torch.is_grad_enabled() and (x.requires_grad or out is not None and out.requires_grad):
-            if out is not None:
-                raise ValueError("out cannot be given where a gradient is recorded")
             _b.check_recorded(x)
+            if out is not None:
+                _b.check_recorded(out)
+                raise ValueError("out cannot be given where a gradient is recorded")
             return _RopeFunction.apply(x, positions, n_new, self, bool(transpose))
         return self._apply(x, positions, n_new, transpose, out)
 
