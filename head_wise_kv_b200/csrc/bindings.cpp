@@ -11,7 +11,9 @@
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <c10/util/SmallVector.h>
+#include <torch/csrc/autograd/functions/accumulate_grad.h>
 #include <torch/csrc/autograd/functions/basic_ops.h>
+#include <torch/csrc/autograd/graph_task.h>
 #include <torch/csrc/autograd/variable.h>
 #include <torch/csrc/jit/frontend/tracer.h>
 #include <torch/extension.h>
@@ -24,6 +26,7 @@
 #include <stdexcept>
 #include <string>
 #include <tuple>
+#include <unordered_set>
 #include <vector>
 
 #include "duo_kv.h"
@@ -86,16 +89,51 @@ void check_not_traced(const char* call) {
 // A backward pass captured into a graph must not meet a leaf whose gradient
 // node lives on another stream (an eager graph of the same leaf keeps it): the
 // engine would make the capture wait for a stream outside it, on a thread of
-// its own, where the error ends the process.  Refused here instead.
-void check_capture(const Tensor& t, const char* name) {
-    if (!t.requires_grad() || !t.is_leaf() || !at::GradMode::is_enabled()) return;
-    if (c10::cuda::currentStreamCaptureStatusMayInitCtx() == c10::cuda::CaptureStatus::None) return;
-    const auto node = torch::autograd::impl::try_get_grad_accumulator(t);
-    if (!node) return;
-    const auto stream = node->stream();
-    TORCH_CHECK_VALUE(!stream || *stream == c10::cuda::getCurrentCUDAStream(t.device().index()).unwrap(), name,
+// its own, where the error ends the process.  Refused here instead: at the
+// forward call where a leaf is its input, in the backward pass where leaves
+// lie further up (parts of a projection, its weights).
+bool capturing_on(const at::Device& dev) {
+    const c10::cuda::OptionalCUDAGuard guard(dev);
+    return c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None;
+}
+
+void check_leaf(torch::autograd::Node& node, const at::Device& dev, const char* name) {
+    const auto stream = node.stream();
+    TORCH_CHECK_VALUE(!stream || *stream == c10::cuda::getCurrentCUDAStream(dev.index()).unwrap(), name,
                       " is a leaf of an eager graph that is still alive: drop that graph, or give the capture a leaf of its "
                       "own, before its backward pass is captured");
+}
+
+void check_capture(const Tensor& t, const char* name) {
+    if (!t.requires_grad() || !t.is_leaf() || !at::GradMode::is_enabled() || !t.is_cuda()) return;
+    if (!capturing_on(t.device())) return;
+    if (const auto node = torch::autograd::impl::try_get_grad_accumulator(t)) check_leaf(*node, t.device(), name);
+}
+
+// In a backward pass on `dev`: the leaves that it will reach from here.
+void check_captured_backward(const at::Device& dev) {
+    if (!capturing_on(dev)) return;
+    const auto start = torch::autograd::get_current_node();
+    const auto* plan = torch::autograd::get_current_graph_task_exec_info();     // empty: every node runs
+    std::vector<torch::autograd::Node*> stack;
+    std::unordered_set<torch::autograd::Node*> seen;
+    const auto follow = [&](const torch::autograd::Node& node) {
+        for (const auto& edge : node.next_edges()) {
+            if (!edge.function || !seen.insert(edge.function.get()).second) continue;
+            if (plan && !plan->empty()) {
+                const auto it = plan->find(edge.function.get());
+                if (it == plan->end() || !it->second.should_execute()) continue;
+            }
+            stack.push_back(edge.function.get());
+        }
+    };
+    if (start) follow(*start);
+    while (!stack.empty()) {
+        torch::autograd::Node* node = stack.back();
+        stack.pop_back();
+        if (dynamic_cast<torch::autograd::AccumulateGrad*>(node)) check_leaf(*node, dev, "what this backward pass reaches");
+        follow(*node);
+    }
 }
 
 cudaStream_t stream_of(const at::Device& dev) { return c10::cuda::getCurrentCUDAStream(dev.index()).stream(); }
@@ -578,6 +616,7 @@ struct WindowAttention : torch::autograd::Function<WindowAttention> {
         const auto saved = ctx->get_saved_variables();
         const Tensor &q = saved[0], &k = saved[1], &v = saved[2], &out = saved[3], &stats = saved[4], &lengths = saved[5];
         const c10::cuda::CUDAGuard guard(q.device());
+        check_captured_backward(q.device());
         torch::autograd::variable_list res(7);
         {
             const at::AutoGradMode off(false);
@@ -676,6 +715,7 @@ PYBIND11_MODULE(TORCH_EXTENSION_NAME, m) {
     });
     m.def("overlap", &overlap);
     m.def("overlaps_itself", &overlaps_itself);
+    m.def("check_captured_backward", [](const Tensor& t) { check_captured_backward(t.device()); });
     m.def("check_recorded", [](const Tensor& t) {       // what an autograd function of Python's checks first
         check_not_traced("Rope.apply");
         check_plain(t, "x");

@@ -93,6 +93,7 @@ class _RopeFunction(torch.autograd.Function):
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, grad):
+        _b.check_captured_backward(grad)
         positions, *rest = ctx.saved_tensors
         if grad.stride(3) != 1 or any(s * grad.element_size() % 16 for s in grad.stride()[:3]) or \
                 grad.data_ptr() % 16:

@@ -549,3 +549,52 @@ def test_status_outlives_the_inference_mode_of_the_first_call():
     import sys
     done = subprocess.run([sys.executable, "-c", _FIRST_IN_INFERENCE], capture_output=True, text=True, timeout=240)
     assert done.returncode == 0, done.stderr[-2000:]
+
+
+_LEAF_FURTHER_UP = """
+import sys
+import torch
+from head_wise_kv_b200 import Rope, window_attention
+rope, pos = Rope(128), torch.zeros(1, dtype=torch.int32, device="cuda:0")
+w = torch.randn(1, 40, 6, 128, device="cuda:0").to(torch.bfloat16).requires_grad_()
+
+def attend(w):
+    return window_attention(*[t.transpose(1, 2) for t in w.split([2, 2, 2], 2)], 2, 9)
+
+def rotate(w):
+    return rope.apply(w.transpose(1, 2), pos)
+
+for f in (attend, rotate):
+    keep = f(w)                     # an eager graph of the leaf
+    for take in (lambda y: torch.autograd.grad(y.float().sum(), w), lambda y: y.float().sum().backward()):
+        graph = torch.cuda.CUDAGraph()
+        try:
+            with torch.cuda.graph(graph):
+                take(f(w))
+        except ValueError as e:
+            assert "eager graph" in str(e), e
+        else:
+            sys.exit("captured")
+        torch.cuda.synchronize()
+    # the forward pass alone may be captured, and so may both with a leaf of the capture's own
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = f(w)
+    graph.replay()
+    assert torch.equal(out, keep)
+    own = w.detach().clone().requires_grad_()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got, = torch.autograd.grad(f(own).float().sum(), own)
+    graph.replay()
+    assert torch.equal(got, torch.autograd.grad(keep.float().sum(), w)[0])
+    del keep, out
+print("done")
+"""
+
+
+def test_captured_backward_that_would_meet_an_eager_graphs_leaf_further_up():
+    import subprocess
+    import sys
+    done = subprocess.run([sys.executable, "-c", _LEAF_FURTHER_UP], capture_output=True, text=True, timeout=240)
+    assert done.returncode == 0 and done.stdout.endswith("done\n"), (done.returncode, done.stderr[-2000:])
