@@ -598,3 +598,24 @@ def test_captured_backward_that_would_meet_an_eager_graphs_leaf_further_up():
     import sys
     done = subprocess.run([sys.executable, "-c", _LEAF_FURTHER_UP], capture_output=True, text=True, timeout=240)
     assert done.returncode == 0 and done.stdout.endswith("done\n"), (done.returncode, done.stderr[-2000:])
+
+
+def test_d_comes_from_the_unrounded_result():
+    """Two keys of one weight whose values are one step apart: the result lies half a step between them, and what its
+    rounding takes away is as large as ds itself.
+
+    v = 1 and 1 + 2e (e half a step, 2^-8 for bf16): out = 1 + e rounds to 1 (to even).  With g = 1 and 128 dims
+    D = 128 (1 + e), ds = -+ 64 e; from the rounded result D = 128 would give 0 and 128 e.  Everything is exact up to
+    the fast exponential (p = 1/2 within 2^-18, so D within 2^-10 and ds within 2^-10) and the rounding of ds."""
+    for dtype in (torch.bfloat16, torch.float16):
+        e = torch.finfo(dtype).eps / 2
+        q, k, v = (torch.zeros(1, 1, 2, 128, dtype=dtype, device=DEV) for _ in range(3))
+        q[..., 1] = 1                       # what dk = scale ds^T q shows
+        k[0, 0, 0, 0], k[0, 0, 1, 1] = 1, 0  # what dq = scale ds k shows
+        v[0, 0, 0], v[0, 0, 1] = 1, 1 + 2 * e
+        got = _run(q, k, v, torch.ones_like(q), 0, None, scale=1.0)
+        assert (got[0][0, 0, 1] == 1).all()
+        ds = [float(got[2][0, 0, 0, 1]), float(got[2][0, 0, 1, 1]), float(got[1][0, 0, 1, 0])]
+        # ds, its rounding and the result's: 64 e is 0.25 or 2^-5, and 2^-10 is 1/256 or 1/32 of it
+        for y, want in zip(ds, (-64 * e, 64 * e, -64 * e)):
+            assert abs(y - want) <= 2.0 ** -10 + 2 * e * 64 * e, (dtype, ds)
