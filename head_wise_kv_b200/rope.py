@@ -29,6 +29,8 @@ class Rope:
         if scaling not in _SCALING:
             raise ValueError(f"scaling must be one of {sorted(_SCALING)}")
         self.handle = None
+        pair_factors = None if pair_factors is None else [float(x) for x in pair_factors]
+        self._made_of = (head_dim, theta, rot_dim, layout, scaling, factor, original_len, low, high, magnitude, pair_factors)
         self.d = int(head_dim)
         self.rot_dim = self.d if rot_dim is None else int(rot_dim)
         if pair_factors is not None and len(pair_factors) != self.rot_dim // 2:
@@ -37,6 +39,10 @@ class Rope:
                                        float(factor), float(original_len), float(low), float(high), float(magnitude),
                                        pair_factors)
         self.handle = L.duo_rope_create(desc)
+
+    def __reduce__(self):
+        # a copy has a plan of its own: this one's is freed once
+        return type(self), self._made_of
 
     def close(self):
         if getattr(self, "handle", None):

@@ -5,6 +5,8 @@ device."""
 import ctypes
 import itertools
 import random
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -213,3 +215,25 @@ def test_overlap_of_a_projections_parts():
     assert not _binding.overlap(k, flat[:1024]) and not _binding.overlap(k, flat[1280:1536])
     assert _binding.overlaps_itself(q.expand(2, 500, 8, 128)[:1, :1].expand(3, 4, 8, 128))
     assert not any(_binding.overlaps_itself(t) for t in (q, k, v, q.transpose(1, 2)))
+
+
+_COPIES = """
+import copy, pickle
+from head_wise_kv_b200 import Rope
+for r in (Rope(128), Rope(64, rot_dim=32, layout="interleaved", scaling="factors", pair_factors=[1.0 + i for i in range(16)]),
+          Rope(128, 500000.0, scaling="yarn", factor=8.0, original_len=4096, low=2.0, high=20.0, magnitude=1.5)):
+    same = [copy.copy(r), copy.deepcopy({"layer": [r]})["layer"][0], pickle.loads(pickle.dumps(r))]
+    want = r.frequencies()
+    for c in same:
+        assert c.handle not in (None, r.handle) and c.frequencies() == want and (c.d, c.rot_dim) == (r.d, r.rot_dim)
+    r.close()
+    assert all(c.frequencies() == want for c in same)
+    same.clear()
+print("done")
+"""
+
+
+def test_copies_of_a_plan_are_plans_of_their_own():
+    """A copied model's Rope: the plan is freed once each (in a process of its own: a second free ends it)."""
+    done = subprocess.run([sys.executable, "-c", _COPIES], capture_output=True, text=True, timeout=240)
+    assert done.returncode == 0 and done.stdout == "done\n", done.stderr[-2000:]
