@@ -168,7 +168,8 @@ class DuoKVCache:
         """Sequence dst continues from the first ``length`` tokens of
         sequence src (every layer).  Paged caches share the pages that the
         page table maps to the same pool page for both; see duo_kv_fork."""
-        L.duo_kv_fork(self.handle, src, dst, length, _stream(self.device))
+        with _on(self.device):
+            L.duo_kv_fork(self.handle, src, dst, length, _stream(self.device))
 
     def check_wait_timeout(self, limit_ns: int):
         """Make one bounded device wait run out (see duo_kv_check_wait_timeout)."""
