@@ -603,3 +603,20 @@ def test_what_a_call_writes_counts_as_changed():
         rope.apply(t, zero, out=t)
     with pytest.raises(ValueError, match="recorded"):
         rope.apply(x[0].detach(), zero, out=x[0])
+
+
+@pytest.mark.parametrize("kind,layout,rot", [("int4", "half", None), ("paged_int4", "interleaved", 64), ("paged_fp8", "half", 32)])
+def test_step_rope_on_quantised_caches(kind, layout, rot):
+    st = Setup(kind, B=4, window=8, layout=layout, rot=rot)
+    lens = torch.tensor([0, 3, 700, 255], dtype=torch.int32, device=DEV)
+    _, k0, v0 = _qkv(st, 0, 21, (4, 700))
+    for c in st.caches:
+        c.append_rope(0, st.rope, None, k0, v0, torch.zeros_like(lens), n_new=lens)
+    for step in range(10):
+        q, k, v = _qkv(st, 4, 30 + step)
+        got, lse = st.caches[0].step_rope(0, st.rope, q, k, v, lens, lens + 1, 0.09, want_lse=True)
+        qr = st.caches[1].append_rope(0, st.rope, q[:, None], k[:, None], v[:, None], lens)[:, 0].contiguous()
+        ref, ref_lse = st.caches[1].decode(0, qr, lens + 1, 0.09, want_lse=True)
+        assert torch.equal(got, ref) and torch.equal(lse, ref_lse) and torch.equal(st.caches[0].buf, st.caches[1].buf)
+        lens = lens + 1
+    assert st.caches[0].status() == st.caches[1].status() == 0

@@ -619,3 +619,28 @@ def test_d_comes_from_the_unrounded_result():
         # ds, its rounding and the result's: 64 e is 0.25 or 2^-5, and 2^-10 is 1/256 or 1/32 of it
         for y, want in zip(ds, (-64 * e, 64 * e, -64 * e)):
             assert abs(y - want) <= 2.0 ** -10 + 2 * e * 64 * e, (dtype, ds)
+
+
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_scores_far_from_zero(sign, dtype):
+    """Every scaled score of a row about +- 2^22, the edge of what is taken: only their differences count.
+
+    127 dims of 2^7 times +- 2^11, and a last one of 2^-1 times +- 2^11 + 16 d_j: fp32 holds the sums (below 2^25, in
+    steps of 2).  Scaled by 2^-3 that is +- 2^22 + d_j.  In log2 units a row's rounding of the maximum is common to its
+    weights, and what is left are differences below 2: weights are right to 2^-17 + u."""
+    from head_wise_kv_b200 import window_attention, window_attention_status
+    T = 300
+    q = torch.full((1, 1, T, 128), 128.0, dtype=dtype, device=DEV)
+    q[..., 127] = 0.5
+    k = torch.full((1, 1, T, 128), sign * 2048.0, dtype=dtype, device=DEV)
+    d = torch.arange(T, device=DEV) % 2
+    k[0, 0, :, 127] = (sign * 2048.0 + d * 16).to(dtype)
+    assert (k[0, 0, :, 127].double() == sign * 2048 + d * 16).all()
+    v = torch.randn(1, 1, T, 128, generator=torch.Generator().manual_seed(1)).to(dtype).to(DEV)
+    got = window_attention(q, k, v, scale=0.125).double()[0, 0]
+    s = (q[0, 0].double() @ k[0, 0].double().T) * 0.125
+    p = torch.softmax(s.masked_fill(~torch.ones(T, T, dtype=torch.bool, device=DEV).tril(), -torch.inf), -1)
+    want, u = p @ v[0, 0].double(), torch.finfo(dtype).eps / 2
+    bound = (u + 2.0 ** -17) * (p @ v[0, 0].double().abs()) + u * want.abs() + 2.0 ** -24
+    assert ((got - want).abs() <= bound).all() and window_attention_status(DEV) == 0
