@@ -5,6 +5,7 @@
 // ctypes cost more than that (8 to 15 us a call, 200 us for a small
 // attention's forward and backward).  Nothing is computed here: every step of
 // the path runs in the library's kernels (duo_kv.h).
+#include <ATen/TracerMode.h>
 #include <ATen/core/grad_mode.h>
 #include <c10/core/InferenceMode.h>
 #include <c10/cuda/CUDAGraphsC10Utils.h>
@@ -15,7 +16,6 @@
 #include <torch/csrc/autograd/functions/basic_ops.h>
 #include <torch/csrc/autograd/graph_task.h>
 #include <torch/csrc/autograd/variable.h>
-#include <torch/csrc/jit/frontend/tracer.h>
 #include <torch/extension.h>
 
 #include <algorithm>
@@ -83,7 +83,7 @@ void mark_written(const Tensor& t) {
 }
 
 void check_not_traced(const char* call) {
-    TORCH_CHECK_NOT_IMPLEMENTED(!torch::jit::tracer::isTracing(), call, " cannot be traced: the trace would hold an empty result");
+    TORCH_CHECK_NOT_IMPLEMENTED(!at::tracer::impl::is_dispatch_enabled(), call, " cannot be traced: the trace would hold an empty result");
 }
 
 // A backward pass captured into a graph must not meet a leaf whose gradient
@@ -106,8 +106,8 @@ void check_leaf(torch::autograd::Node& node, const at::Device& dev, const char* 
 
 void check_capture(const Tensor& t, const char* name) {
     if (!t.requires_grad() || !t.is_leaf() || !at::GradMode::is_enabled() || !t.is_cuda()) return;
-    if (!capturing_on(t.device())) return;
-    if (const auto node = torch::autograd::impl::try_get_grad_accumulator(t)) check_leaf(*node, t.device(), name);
+    const auto node = torch::autograd::impl::try_get_grad_accumulator(t);
+    if (node && capturing_on(t.device())) check_leaf(*node, t.device(), name);
 }
 
 // In a backward pass on `dev`: the leaves that it will reach from here.

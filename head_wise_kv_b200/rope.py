@@ -77,7 +77,7 @@ class Rope:
         where out is new).  transpose: the transposed map, i.e. the gradient.
         out may be x (in place).  Differentiable in x (backward mode) where
         out is not given."""
-        if torch.is_grad_enabled() and (x.requires_grad or out is not None and out.requires_grad):
+        if (x.requires_grad or out is not None and out.requires_grad) and torch.is_grad_enabled():
             _b.check_recorded(x)
             if out is not None:
                 _b.check_recorded(out)
