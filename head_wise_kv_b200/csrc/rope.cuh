@@ -19,10 +19,12 @@ struct duo_rope {
 namespace duo {
 
 // A pair's angle at position p is p * f.  As a fraction of a turn in 64-bit
-// fixed point the product wraps modulo whole turns by itself, so the sine of
-// a far position is as exact as that of a near one (f's own rounding, 2^-65
-// turns, times |p| < 2^31 stays below 2^-34 turns; an fp32 angle at position
-// 2^17 would be off by 2^-7 radians).
+// fixed point the product wraps modulo whole turns by itself and adds no
+// rounding of its own.  The fraction comes from a double, f / 2 pi within
+// 2^-54 turns (f <= 1; thetas from 1.5 to 10^6 measured within 2^-55), so the
+// angle is off by at most 2^-54 |p| turns: below fp32's rounding of what is
+// left of it (2^-27 turns) up to |p| = 2^27, and 2^-23 turns, 7.5e-7 radians,
+// at 2^31.  An fp32 angle at position 2^17 would be off by 2^-7 radians.
 struct RopeTable {
     uint64_t turn[64];
     float magnitude;
@@ -62,8 +64,8 @@ __device__ __forceinline__ RopeUnit rope_unit(const RopeTable& t, int u) {
 
 // Cosine and sine, times the magnitude, of a pair at position p.  The nearest
 // quarter turn is taken off in fixed point, so that what becomes fp32 is at
-// most 1/8 of a turn: its rounding moves the angle by at most 2^-25 of itself,
-// below the rounding of the sine.
+// most 1/8 of a turn: its rounding moves the angle by at most 2^-24 of itself,
+// about the rounding of the sine.
 __device__ __forceinline__ void rope_angle(const RopeTable& t, int pair, int p, float sign, float& c, float& s) {
     const uint64_t a = uint64_t(int64_t(p)) * t.turn[pair];
     const uint32_t quarter = uint32_t((a + (uint64_t(1) << 61)) >> 62);

@@ -527,9 +527,10 @@ typedef struct {
  *     sequence b at positions[b] + i; else [batch][n];
  *   n_new: device int32 [batch] or NULL: only the first n_new[b] tokens of a
  *     sequence are read and written, the rest of out stays as it was.
- * Arithmetic is fp32, rounded once; angles are exact multiples of a turn in
- * 64-bit fixed point, so far positions lose nothing.  Runs on the current
- * device, which holds every tensor. */
+ * Arithmetic is fp32, rounded once.  Angles are multiples of a turn in 64-bit
+ * fixed point, off by at most 2^-54 |p| turns at position p (angles per
+ * position up to 1): below fp32's own rounding up to 2^27, 7.5e-7 radians at
+ * 2^31.  Runs on the current device, which holds every tensor. */
 DUO_API int duo_rope_apply(const duo_rope* rope, int32_t dtype, int32_t transpose, int32_t batch, int32_t n,
                            const duo_rope_tensor* tensors, int32_t num_tensors, const int32_t* positions,
                            int32_t per_token, const int32_t* n_new, duo_stream_t stream);
