@@ -19,9 +19,10 @@ def window_attention(q, k, v, sink=0, window=None, lengths=None, scale=None):
     j < sink or j > i - window; window None: all of them.  lengths: int32
     [batch], tokens of each sequence (default all); results behind them are
     zero, and what the inputs hold there does not matter.  scale: default
-    128 ** -0.5.  The result has q's order of dimensions; gradients have their
-    inputs'.  Differentiable once, in backward mode.  To capture a backward
-    pass into a graph, capture its forward pass with it.  See duo_window_attn."""
+    128 ** -0.5; scores, scale |q.k|, stay below 2^23.  The result has q's
+    order of dimensions; gradients have their inputs'.  Differentiable once,
+    in backward mode.  To capture a backward pass into a graph, capture its
+    forward pass with it.  See duo_window_attn."""
     return _b.window_attention(q, k, v, sink, window, lengths, scale)
 
 
