@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, 4) append_rope_kernel(const __grid_c
         // a map whose lengths have advanced in place (len_before is len_after) still says by its token 0 that
         // the sequence starts from empty
         if (lead && pos == 0 && p.map_seq && p.len_before[b] != 0)
-            for (int r = p.len_after[b]; r < SW; ++r) p.pos[size_t(b) * SW + r] = -1;
+            for (int r = max(p.len_after[b], 1); r < SW; ++r) p.pos[size_t(b) * SW + r] = -1;      // whatever a map says
     }
 
     for (int x = threadIdx.x; x < kTokens * kPairs; x += kThreads) {

@@ -620,3 +620,26 @@ def test_step_rope_on_quantised_caches(kind, layout, rot):
         assert torch.equal(got, ref) and torch.equal(lse, ref_lse) and torch.equal(st.caches[0].buf, st.caches[1].buf)
         lens = lens + 1
     assert st.caches[0].status() == st.caches[1].status() == 0
+
+
+def test_a_map_with_a_negative_length_stays_within_the_ring():
+    """Token 0 of a sequence whose len_after is not one: nothing before the sequence's slots is written."""
+    from head_wise_kv_b200 import TokenMap
+    st = Setup("bf16", caches=1)
+    c = st.caches[0]
+    c.buf[4096:].fill_(7)
+    m = TokenMap(3, 2, DEV)
+    m.seq[0], m.pos[0] = 0, 0
+    m.len_after.copy_(torch.tensor([-30, 0, 0]))
+    _, k, v = _qkv(st, 2, 5)
+    keep = {n: t.clone() for n, t in c.layer_views(0).items() if torch.is_tensor(t)}
+    c.append_rope(0, st.rope, None, k, v, torch.tensor([9, 9, 9], dtype=torch.int32, device=DEV), m)
+    views = c.layer_views(0)
+    SW = st.S + st.W
+    assert torch.equal(views["positions"][1:], keep["positions"][1:])
+    assert views["positions"][0].tolist() == [0] + [-1] * (SW - 1)
+    for name, at in (("k_retrieval", (0, slice(None), 0)), ("v_retrieval", (0, slice(None), 0)), ("k_streaming", (0, slice(None), 0)),
+                     ("v_streaming", (0, slice(None), 0))):
+        mask = torch.ones(keep[name].shape[:3], dtype=torch.bool, device=DEV)
+        mask[at] = False
+        assert _same(views[name][mask], keep[name][mask]), name
