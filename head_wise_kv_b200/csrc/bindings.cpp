@@ -87,11 +87,12 @@ void check_not_traced(const char* call) {
 }
 
 // A backward pass captured into a graph must not meet a leaf whose gradient
-// node lives on another stream (an eager graph of the same leaf keeps it): the
-// engine would make the capture wait for a stream outside it, on a thread of
-// its own, where the error ends the process.  Refused here instead: at the
-// forward call where a leaf is its input, in the backward pass where leaves
-// lie further up (parts of a projection, its weights).
+// node lives on the default stream (an eager graph of the same leaf keeps it):
+// the engine would make the capture wait for that stream, which cannot join
+// it, on a thread of its own, where the error ends the process.  Refused here
+// instead: at the forward call where a leaf is its input, in the backward pass
+// where leaves lie further up (parts of a projection, its weights).  Another
+// stream joins the capture, as that of the warm-up before it does.
 bool capturing_on(const at::Device& dev) {
     const c10::cuda::OptionalCUDAGuard guard(dev);
     return c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None;
@@ -99,7 +100,7 @@ bool capturing_on(const at::Device& dev) {
 
 void check_leaf(torch::autograd::Node& node, const at::Device& dev, const char* name) {
     const auto stream = node.stream();
-    TORCH_CHECK_VALUE(!stream || *stream == c10::cuda::getCurrentCUDAStream(dev.index()).unwrap(), name,
+    TORCH_CHECK_VALUE(!stream || *stream != c10::cuda::getDefaultCUDAStream(dev.index()).unwrap(), name,
                       " is a leaf of an eager graph that is still alive: drop that graph, or give the capture a leaf of its "
                       "own, before its backward pass is captured");
 }

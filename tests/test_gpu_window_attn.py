@@ -644,3 +644,66 @@ def test_scores_far_from_zero(sign, dtype):
     want, u = p @ v[0, 0].double(), torch.finfo(dtype).eps / 2
     bound = (u + 2.0 ** -17) * (p @ v[0, 0].double().abs()) + u * want.abs() + 2.0 ** -24
     assert ((got - want).abs() <= bound).all() and window_attention_status(DEV) == 0
+
+
+_CAPTURED_AFTER_WARM_UP = """
+import torch
+from torch import nn
+from head_wise_kv_b200 import Rope, window_attention, window_attention_status
+
+class Layer(nn.Module):
+    def __init__(self):
+        super().__init__()
+        self.proj = nn.Linear(256, 8 * 128, bias=False, dtype=torch.bfloat16, device="cuda")
+        self.rope = Rope(128)
+        self.register_buffer("pos", torch.zeros(2, dtype=torch.int32, device="cuda"))
+
+    def forward(self, x):
+        q, k, v = (t.transpose(1, 2) for t in self.proj(x).view(2, -1, 8, 128).split([4, 2, 2], 2))
+        return window_attention(self.rope.apply(q, self.pos), self.rope.apply(k, self.pos), v, 4, 50)
+
+torch.manual_seed(0)
+layer = Layer()
+x = torch.randn(2, 130, 256, device="cuda", dtype=torch.bfloat16)
+
+def step(f):
+    f(x).float().square().sum().backward()
+    grad, layer.proj.weight.grad = layer.proj.weight.grad, None
+    return grad
+
+want = step(layer)
+# forward and backward captured apart, the warm-up's gradient nodes kept on a stream of its own
+assert torch.equal(step(torch.cuda.make_graphed_callables(layer, (x.clone(),))), want)
+del layer.forward
+# a whole step, warmed up on a side stream whose last graph is kept
+side = torch.cuda.Stream()
+side.wait_stream(torch.cuda.current_stream())
+with torch.cuda.stream(side):
+    step(layer)
+    keep = layer(x)
+torch.cuda.current_stream().wait_stream(side)
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    layer(x).float().square().sum().backward()
+layer.proj.weight.grad.zero_()
+graph.replay()
+assert torch.equal(layer.proj.weight.grad, want) and window_attention_status("cuda") == 0
+# a leaf as the call's own input
+q, k, v = (torch.randn(1, 2, 40, 128, device="cuda").to(torch.bfloat16).requires_grad_() for _ in range(3))
+with torch.cuda.stream(side):
+    keep = window_attention(q, k, v, 2, 9)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = torch.autograd.grad(window_attention(q, k, v, 2, 9).float().square().sum(), (q, k, v))
+graph.replay()
+assert all(torch.equal(a, b) for a, b in zip(got, torch.autograd.grad(keep.float().square().sum(), (q, k, v))))
+print("done")
+"""
+
+
+def test_captures_after_a_warm_up_on_another_stream():
+    import subprocess
+    import sys
+    done = subprocess.run([sys.executable, "-c", _CAPTURED_AFTER_WARM_UP], capture_output=True, text=True, timeout=240)
+    assert done.returncode == 0 and done.stdout.endswith("done\n"), (done.returncode, done.stderr[-2000:])
