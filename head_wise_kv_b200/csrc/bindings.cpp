@@ -83,7 +83,8 @@ void mark_written(const Tensor& t) {
 }
 
 void check_not_traced(const char* call) {
-    TORCH_CHECK_NOT_IMPLEMENTED(!at::tracer::impl::is_dispatch_enabled(), call, " cannot be traced: the trace would hold an empty result");
+    TORCH_CHECK_NOT_IMPLEMENTED(!at::tracer::impl::is_dispatch_enabled(), call,
+                                " cannot be traced: the trace would hold an empty result");
 }
 
 // A backward pass captured into a graph must not meet a leaf whose gradient

@@ -1028,7 +1028,8 @@ __device__ __forceinline__ void key_tile(const WindowAttnParams& p, Bars& sh, ui
                                     (cb + c * 32) / 4 * kTile + r;
 #pragma unroll
                         for (int z = 0; z < 32; z += 4)
-                            y[z / 4 * kTile] = row ? make_float4(__uint_as_float(o[z]) * held[w], __uint_as_float(o[z + 1]) * held[w],
+                            y[z / 4 * kTile] = row ? make_float4(__uint_as_float(o[z]) * held[w],
+                                                                 __uint_as_float(o[z + 1]) * held[w],
                                                                  __uint_as_float(o[z + 2]) * held[w],
                                                                  __uint_as_float(o[z + 3]) * held[w])
                                                    : make_float4(0.f, 0.f, 0.f, 0.f);
